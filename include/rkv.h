@@ -15,6 +15,16 @@
  *                        pinned prefix of first frames);
  *                        kvcache_ring_update_rope rotates K on the way in
  *
+ * and, for streams of which only a window or a budget of tokens is kept:
+ *
+ *   attn_fwd_window      attn_fwd_varlen with a sliding window and first blocks
+ *                        that stay visible, grouped heads
+ *   attn_decode_paged    attention of the newest tokens over a paged cache,
+ *                        optionally adding up the weight each token received
+ *   kvcache_paged_insert / kvcache_paged_evict
+ *                        write new tokens into the pages; drop the tokens that
+ *                        received the least attention
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - Tensors are bfloat16, token-major [L][H][D] ("row" = one token, H heads
@@ -353,6 +363,64 @@ rkv_status attn_fwd_varlen_noalloc(const rkv_attn_seq* seqs, int32_t n_seqs, int
 rkv_status rkv_attn_noalloc_status(void* stream);
 
 /*
+ * attn_fwd_window -- attn_fwd_varlen with a sliding window and first blocks
+ * that stay visible ("sinks"), and with grouped heads.
+ *
+ * The pages describe a window of frames that slides over the stream ("Amazon
+ * and Reactor tune Trainium for real-time video generation", section "Three
+ * problems for generic compilers"); this call applies that window as a mask
+ * where the keys of older frames are still in the context.
+ *
+ *   seqs, n_seqs, softmax_scale, rope, workspace, workspace_bytes, stream
+ *                  as for attn_fwd_varlen (same workspace size, same status
+ *                  word, rkv_attn_status), with block_frames >= 1 in every
+ *                  sequence.  A frame grid of 1 x 1 makes a block of
+ *                  block_frames tokens: block_frames = 1 is the causal mask
+ *                  by token.
+ *   windows        host array of n_seqs masks.  With B = block_frames * F
+ *                  tokens per block, qb the block of a query row and kb that
+ *                  of a key (counted from key frame 0, as in attn_fwd_varlen),
+ *                  the key is visible iff kb <= qb and
+ *                  (window_blocks == 0 or kb > qb - window_blocks or
+ *                   kb < sink_blocks).
+ *                  window_blocks = 0 is attn_fwd_varlen's mask.
+ *   H, H_kv        query heads and key heads, H a multiple of H_kv; query
+ *                  head h reads key head h / (H / H_kv).  k and v are
+ *                  [Lk][H_kv][D] with row strides >= H_kv * D.
+ * Work follows the mask: a 512-row unit reads the key tiles of the sinks and
+ * of its rows' windows only.  A query row that sees no key gets zeros.  Keys
+ * that no row of a unit sees never reach its outputs, whatever they hold; a V
+ * row that some rows of a unit see and others do not must be finite, because
+ * its product with a weight of zero enters the others' sums.
+ * Errors: those of attn_fwd_varlen, plus RKV_ERR_INVALID_ARG for NULL windows,
+ * block_frames < 1, window_blocks or sink_blocks < 0, H not a multiple of H_kv.
+ */
+typedef struct {
+  int32_t window_blocks; /* blocks a row sees, its own included; 0 = all      */
+  int32_t sink_blocks;   /* first blocks that stay visible                    */
+} rkv_attn_window;
+
+rkv_status attn_fwd_window(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
+                           int32_t H_kv, int32_t D, float softmax_scale, const rkv_rope3d* rope, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * rkv_attn_window_rows -- the mask and key-tile plan attn_fwd_window would
+ * use, evaluated on the host by the same functions the kernel compiles (as
+ * rkv_attn_mask_rows; needs no GPU).  Query row r sees the keys
+ * [0, row_sink[r]) and [row_begin[r], row_limit[r]).
+ *
+ *   seqs, windows, n_seqs, H, rope   as for attn_fwd_window; only Lq, Lk,
+ *                  q_frame_offset, block_frames and the frame grid are read
+ *   row_sink, row_begin, row_limit   host int64 [sum of Lq] each, rows of the
+ *                  sequences one after another in the order given
+ *   unit_tiles, n_units   as for rkv_attn_mask_rows
+ */
+rkv_status rkv_attn_window_rows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
+                                const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
+                                int32_t* unit_tiles, int64_t* n_units);
+
+/*
  * Per-layer rolling KV cache.
  *
  * Source: every layer reads and writes a rolling KV cache, and frames are
@@ -486,14 +554,169 @@ rkv_status rkv_ring_status(void* stream);
  * frame or the ring is malformed. */
 int32_t rkv_ring_slot(const rkv_ring* ring, int32_t logical_frame);
 
+/*
+ * Paged KV cache of several token streams.
+ *
+ * The pages' caches hold whole frames of one stream in order ("Amazon and
+ * Reactor tune Trainium for real-time video generation", section "Three
+ * problems for generic compilers"); this is the form for streams that grow by
+ * one token or a few at a time, each to its own length: keys and values live in
+ * pages of a common pool and a table lists each stream's pages.  The buffers of
+ * an rkv_ring are such a pool (a slot is a page of tokens_per_frame tokens).
+ *
+ *   k, v           device bf16, n_pages pages of [page_tokens][H][D]
+ *   page_stride    elements between consecutive pages of k, and of v:
+ *                  >= page_tokens * H * D and a multiple of D (k and v may be
+ *                  the two halves of one [n_pages][2][...] tensor)
+ *   page_tokens    tokens per page, any number >= 1
+ *   page_table     device int32 [n_seqs][max_pages], table_stride entries
+ *                  between rows: token j of sequence s is row
+ *                  j % page_tokens of page page_table[s][j / page_tokens].
+ *                  Entries past a sequence's length are not read.  Sequences
+ *                  may share pages that are only read.
+ *   status         device int32 the calls below record device-side findings
+ *                  in (rkv_paged_status), zeroed by the caller once; or NULL
+ * A sequence's capacity is max_pages * page_tokens tokens.
+ *
+ * Lengths are on the device, so one captured launch serves a growing stream:
+ *   seq_lens       device int32 [n_seqs], tokens of each sequence, those a
+ *                  call inserts or attends from included; 0 is an empty
+ *                  (padded) sequence
+ * Nothing of this can be checked on the host, so the kernels do: a length
+ * below 0 counts as 0, one above the capacity as the capacity, and a token on
+ * a page outside [0, n_pages) is not read, not written and not visible.  Each
+ * records RKV_ERR_DEVICE_CHECK in `status`.
+ *
+ * Scores, one fp32 weight and one int32 position per token and key head:
+ *   weight         device fp32 [n_seqs][H][capacity], the attention weight the
+ *                  token received so far (attn_decode_paged adds to it)
+ *   pos            device int32 [n_seqs][H][capacity], the token's position in
+ *                  its stream (evictions change the order of a head's tokens)
+ *   next_pos       device int32 [n_seqs], the position after the newest token
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t H; /* key heads */
+  int32_t D;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t* status;
+} rkv_paged_cache;
+
+/*
+ * kvcache_paged_insert -- write the newest n_new tokens of every sequence.
+ *
+ *   k_new, v_new   device bf16 [n_seqs * n_new][H][D], sequence by sequence,
+ *                  row stride new_row_stride (elements); must not overlap the
+ *                  pool.  Keys as the attention is to read them (rotated).
+ *   n_new          tokens per sequence, >= 0 (0 = no-op)
+ *   seq_lens       lengths with the new tokens included: row i of sequence s
+ *                  becomes token seq_lens[s] - n_new + i; rows that fall
+ *                  before token 0 (a padded or shorter sequence) are skipped
+ *   pos, next_pos  optional (both or neither): pos[s][h][token] =
+ *                  next_pos[s] - n_new + i, next_pos with the new tokens
+ *                  included
+ *   weight         optional: weight[s][h][token] = 0
+ * Two sequences must not insert into the same page.
+ * Errors: RKV_ERR_INVALID_ARG (cache, pointers, strides, overlap, n_new < 0 or
+ * above the capacity), RKV_ERR_UNSUPPORTED (2^31 or more 16-byte pieces).
+ */
+rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const void* k_new, const void* v_new,
+                                int64_t new_row_stride, int32_t n_new, const int32_t* seq_lens,
+                                const int32_t* next_pos, int32_t* pos, float* weight, void* stream);
+
+/*
+ * attn_decode_paged -- attention of the newest Lq tokens of every sequence
+ * over its pages, split over the cache's length and joined.
+ *
+ *   q, o           device bf16 [n_seqs * Lq][Hq][D], row strides in elements;
+ *                  o may not overlap q, the pool or the other outputs
+ *   Lq             query tokens per sequence, 1 .. RKV_DECODE_MAX_LQ; query i
+ *                  is token c = seq_lens[s] - Lq + i
+ *   Hq             query heads, a multiple of cache->H (query head h reads key
+ *                  head h / (Hq / H))
+ *   window, sinks  token j <= c is visible iff window == 0 or j > c - window
+ *                  or j < sinks (indices in the cache)
+ *   weight_in, weight_out   NULL, or weight_out[s][h][j] = weight_in[s][h][j]
+ *                  + sum over the queries and the query heads of key head h of
+ *                  their softmax weight of token j, for j < seq_lens[s]; the
+ *                  rest of weight_out is left as it was.  weight_in NULL counts
+ *                  as zeros; weight_out may be weight_in, otherwise the two may
+ *                  not overlap.
+ *   workspace      device memory, 16-byte aligned, not used by another call
+ *                  in flight, at least
+ *                  attn_decode_paged_workspace_size(cache, Hq, Lq, weights)
+ *                  bytes (weights: with weight_out).  Needs no initial value.
+ * A query that sees no token gets zeros.  bf16 operands, fp32 scores, softmax
+ * and sums, P rounded to bf16 for its product with V; weights in fp32.  Keys
+ * and values no query of a sequence sees may hold anything; a V row that some
+ * queries of a sequence see and others do not must be finite.  Results do not
+ * depend on timing (no atomics in any sum).
+ * Errors: RKV_ERR_INVALID_ARG (cache, shapes, pointers, alignment, overlap,
+ * workspace), RKV_ERR_UNSUPPORTED (sizes past 32-bit work counts).
+ */
+#define RKV_DECODE_MAX_LQ 64
+
+size_t attn_decode_paged_workspace_size(const rkv_paged_cache* cache, int32_t Hq, int32_t Lq, int32_t weights);
+rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void* q, void* o, int64_t q_row_stride,
+                             int64_t o_row_stride, int32_t Hq, int32_t Lq, const int32_t* seq_lens, float softmax_scale,
+                             int32_t window, int32_t sinks, const float* weight_in, float* weight_out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * kvcache_paged_evict -- cut every sequence to `budget` tokens per key head,
+ * dropping those that received the least attention.
+ *
+ * Per sequence s and key head h with L = seq_lens[s] > budget: tokens with
+ * pos < sinks or pos >= next_pos[s] - recent are kept first, then those of the
+ * largest weight (NaN below every number, -0 equal to 0, ties to the lowest
+ * index), budget in all.  Kept tokens below index `budget` stay where they are;
+ * the others move, in order, into the places of dropped tokens below `budget`,
+ * in order: K and V rows, weight and pos.  A head's tokens are then the indices
+ * [0, budget), in no particular order; the attention over them does not depend
+ * on it.  Each head keeps its own tokens.  L <= budget: the sequence is left
+ * as it is.
+ *
+ *   seq_lens_out   min(L, budget); may be seq_lens
+ *   weight_out, pos_out   the scores of the indices [0, min(L, budget)) after
+ *                  the moves; may be weight / pos (both or neither), otherwise
+ *                  they may not overlap them.  The rest is left as it was.
+ *   budget         >= 1, sinks, recent >= 0
+ *   workspace      as for attn_decode_paged,
+ *                  kvcache_paged_evict_workspace_size(cache, budget) bytes
+ * A sequence whose pages hold tokens outside the pool keeps those tokens'
+ * rows unmoved (status records it).  Sequences must not share pages.
+ * Errors: RKV_ERR_INVALID_ARG (cache, pointers, overlap, sizes, workspace).
+ */
+size_t kvcache_paged_evict_workspace_size(const rkv_paged_cache* cache, int32_t budget);
+rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const int32_t* seq_lens, const float* weight,
+                               const int32_t* pos, const int32_t* next_pos, int32_t budget, int32_t sinks,
+                               int32_t recent, int32_t* seq_lens_out, float* weight_out, int32_t* pos_out,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * rkv_paged_status -- synchronise `stream` and report whether a call on the
+ * cache met a length or a page out of range since the last report:
+ * RKV_ERR_DEVICE_CHECK (the word is then cleared) or RKV_OK.  Errors:
+ * RKV_ERR_INVALID_ARG for a cache without a status word, RKV_ERR_CUDA.
+ */
+rkv_status rkv_paged_status(const rkv_paged_cache* cache, void* stream);
+
 /* Text of the last error returned on the calling thread ("" if none). */
 const char* rkv_last_error_string(void);
 
 /* Library version, major*10000 + minor*100 + patch.  A caller compiled
  * against this header can compare it with RKV_VERSION: the structs above
  * changed layout between minor versions (rkv_ring gained `pinned`,
- * rkv_rope3d its per-axis bases and layout in 0.2). */
-#define RKV_VERSION 200
+ * rkv_rope3d its per-axis bases and layout in 0.2; 0.3 adds the windowed and
+ * the paged calls and changes no struct). */
+#define RKV_VERSION 300
 int32_t rkv_version(void);
 
 #ifdef __cplusplus

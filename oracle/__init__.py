@@ -21,6 +21,8 @@ definition states:
   optionally with the mask.
 * ``ring``      – the per-layer rolling KV cache that inserts and evicts whole
   frames.
+* ``paged``     – token streams over a paged cache: attention of the newest
+  tokens, the weight each cached token received, eviction by it.
 
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*.py``
 against closed forms, invariants, library routines or brute force.
@@ -31,15 +33,17 @@ from .rope3d import (
     AXIS_T, AXIS_H, AXIS_W,
     token_positions, pair_axes, rope_angles, rope3d_ref,
 )
-from .mask import frame_block_visible, frame_pair_visible, default_q_frame_offset
+from .mask import frame_block_visible, frame_pair_visible, frame_window_visible, default_q_frame_offset
 from .attention import attention_ref, attention_rows_ref, fused_attention_ref
 from .ring import RingRef
+from .paged import token_visible, decode_ref, received_weight, evict_moves
 
 __all__ = [
     "bf16_bits_to_f64", "f64_to_bf16_bits", "bf16_ulp_distance",
     "AXIS_T", "AXIS_H", "AXIS_W",
     "token_positions", "pair_axes", "rope_angles", "rope3d_ref",
-    "frame_block_visible", "frame_pair_visible", "default_q_frame_offset",
+    "frame_block_visible", "frame_pair_visible", "frame_window_visible", "default_q_frame_offset",
     "attention_ref", "attention_rows_ref", "fused_attention_ref",
     "RingRef",
+    "token_visible", "decode_ref", "received_weight", "evict_moves",
 ]

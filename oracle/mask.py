@@ -43,3 +43,17 @@ def frame_block_visible(Lq, Lk, frame_tokens, q_frame_offset, block_frames, rows
     qf = q_frame_offset + rows // frame_tokens
     kf = np.arange(Lk, dtype=np.int64) // frame_tokens
     return (kf[None, :] // block_frames) <= (qf[:, None] // block_frames)
+
+
+def frame_window_visible(Lq, Lk, frame_tokens, q_frame_offset, block_frames, window_blocks, sink_blocks, rows=None):
+    """frame_block_visible with a sliding window: of the blocks up to its own a
+    row sees the last ``window_blocks`` (0 = all) and the first ``sink_blocks``."""
+    if rows is None:
+        rows = np.arange(Lq, dtype=np.int64)
+    rows = np.asarray(rows, dtype=np.int64)
+    qb = ((q_frame_offset + rows // frame_tokens) // block_frames)[:, None]
+    kb = (np.arange(Lk, dtype=np.int64) // frame_tokens // block_frames)[None, :]
+    seen = kb <= qb
+    if window_blocks > 0:
+        seen &= (kb > qb - window_blocks) | (kb < sink_blocks)
+    return seen

@@ -115,6 +115,7 @@ struct SeqDev {
   int64_t o_stride_bytes;
   int32_t Lq, Lk, q_t0, k_t0, q_frame_offset, block_frames;
   uint32_t flags;
+  int32_t window_blocks, sink_blocks;   // attn_fwd_window: 0 blocks = no window
   int32_t n_qblocks;
   int32_t unit_begin;
   int64_t stats_row0;   // debug launches: first row of this sequence in row_stats
@@ -123,6 +124,8 @@ struct SeqDev {
 struct Params {
   SeqDev seq[RKV_MAX_SEQS];
   int32_t n_seqs, H;
+  int32_t windowed;   // the launch is attn_fwd_window's
+  int32_t group;      // query heads to a key head (1 unless windowed)
   // work items: units [0, n_whole) whole, then each of the remaining
   // n_split units as two items over the first and second half of its key
   // tiles, whose partial results go to part_o / part_ml
@@ -288,6 +291,10 @@ struct Unit {
   int si, head, qb, nkt;
   int kt0, kt1;   // key tiles [kt0, kt1) of this work item
   int part;       // -1: whole unit; else index of the item's partial-result slot
+  // windowed launches list the key tiles of the sinks and of the window: entry
+  // j of the list is tile j below `ns` and tile j + skip from there on
+  int ns, skip;
+  int32_t lo, sink, hi;   // keys some row of the unit sees: [0, sink) and [lo, hi)
 };
 
 // Keys [0, limit) of the sequence are visible to query row `row`: the whole
@@ -302,10 +309,57 @@ __host__ __device__ __forceinline__ int64_t row_kv_limit(const SeqDev& s, const 
   return lim < s.Lk ? lim : s.Lk;
 }
 
+// Windowed launches: of the keys up to row_kv_limit, a row sees those from
+// row_kv_begin on and the first `row_kv_sink`.
+__host__ __device__ __forceinline__ int64_t row_kv_begin(const SeqDev& s, const Params& p, int row) {
+  if (s.window_blocks <= 0) return 0;
+  const int64_t qf = int64_t(s.q_frame_offset) + row / int64_t(p.F);
+  const int64_t first = qf / s.block_frames - s.window_blocks + 1;
+  if (first <= 0) return 0;
+  const int64_t lo = first * s.block_frames * int64_t(p.F);
+  return lo < s.Lk ? lo : s.Lk;
+}
+__host__ __device__ __forceinline__ int64_t row_kv_sink(const SeqDev& s, const Params& p, int row) {
+  const int64_t lim = row_kv_limit(s, p, row);
+  const int64_t sink = int64_t(s.sink_blocks) * s.block_frames * int64_t(p.F);
+  return sink < lim ? sink : lim;
+}
+
+// The key tiles of a windowed unit (rows [first, last] of its sequence): those
+// of the sinks, then those of the window, or one run where the two meet.
+__host__ __device__ __forceinline__ void window_tiles(const SeqDev& s, const Params& p, int first, int last, Unit& r) {
+  // limits and begins grow with the row, so the first row's begin and the last
+  // row's limit bound the unit
+  r.hi = int32_t(row_kv_limit(s, p, last));
+  r.lo = int32_t(row_kv_begin(s, p, first));
+  r.sink = int32_t(row_kv_sink(s, p, last));
+  r.ns = (r.sink + kBN - 1) / kBN;
+  int w0 = r.lo / kBN, w1 = r.hi > r.lo ? (r.hi + kBN - 1) / kBN : w0;
+  if (r.ns >= w0) {
+    w1 = w1 > r.ns ? w1 : r.ns;
+    r.ns = 0;
+    w0 = 0;
+  }
+  r.skip = w0 - r.ns;
+  r.nkt = r.ns + w1 - w0;
+  if (r.nkt < 1) {   // no row sees a key: one tile, hidden from all of them
+    r.ns = r.skip = 0;
+    r.nkt = 1;
+  }
+}
+
+// Key tile at entry j of a unit's list.
+template <bool kWindow>
+__device__ __forceinline__ int tile_at(const Unit& u, int j) {
+  if constexpr (kWindow) return j < u.ns ? j : j + u.skip;
+  return j;
+}
+
 // Units (512 query rows, one per CTA pair) are numbered head-major within a
 // sequence (all query blocks of head 0, then head 1, ...), so the clusters in
 // flight at any time share the K/V tiles of one or two heads in L2.  Masked
 // sequences list their query blocks from the most to the least visible keys.
+template <bool kWindow>
 __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) {
   Unit r;
   int u = item;
@@ -324,8 +378,12 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
   r.qb = s.block_frames > 0 ? (s.n_qblocks - 1 - ord) : ord;
   int last = (r.qb + 1) * kUnitRows - 1;
   if (last > s.Lq - 1) last = s.Lq - 1;
-  const int64_t kv = row_kv_limit(s, p, last);
-  r.nkt = int((kv + kBN - 1) / kBN);
+  if constexpr (kWindow) {
+    window_tiles(s, p, r.qb * kUnitRows, last, r);
+  } else {
+    const int64_t kv = row_kv_limit(s, p, last);
+    r.nkt = int((kv + kBN - 1) / kBN);
+  }
   r.kt0 = 0;
   r.kt1 = r.nkt;
   if (r.part >= 0) {
@@ -333,6 +391,11 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
     else r.kt1 = r.nkt / 2;
   }
   return r;
+}
+
+// decode_unit on the host, for either kind of launch.
+static Unit host_unit(const Params& p, int item) {
+  return p.windowed ? decode_unit<true>(p, item) : decode_unit<false>(p, item);
 }
 
 __device__ __forceinline__ int pick3(int a, int x, int y, int z) { return a == 0 ? x : (a == 1 ? y : z); }
@@ -582,7 +645,10 @@ __device__ __forceinline__ void setmaxnreg_dec_producer() {
 // kDebug: the instantiation behind attn_fwd_varlen_debug, which also records
 // per-row mask statistics and can skip one handoff (stall injection); the
 // production instantiations compile neither.
-template <int kPT, int kPH, bool kHalf, bool kDebug>
+// kWindow: attn_fwd_window's instantiation, which lists the key tiles of the
+// sinks and the window, hides keys on both sides of each row's window, and
+// reads the key head of the query head's group.
+template <int kPT, int kPH, bool kHalf, bool kDebug, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -673,10 +739,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const float scale_log2 = p.scale_log2;
     uint32_t g = 0, items = 0;
     for (int k = 0; k < n_items; ++k, ++items) {
-      const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+      const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
       const SeqDev& s = p.seq[un.si];
       const int qrow = un.qb * kUnitRows + int(rank) * kCtaRows + wg * kBM + 32 * (warp & 3) + lane;
       const int64_t my_limit = row_kv_limit(s, p, qrow < s.Lq ? qrow : s.Lq - 1);
+      int32_t my_lo = 0, my_sink = 0;   // windowed: the row sees [0, my_sink) and [my_lo, my_limit)
+      if constexpr (kWindow) {
+        my_lo = int32_t(row_kv_begin(s, p, qrow < s.Lq ? qrow : s.Lq - 1));
+        my_sink = int32_t(row_kv_sink(s, p, qrow < s.Lq ? qrow : s.Lq - 1));
+        if (my_sink >= my_lo) my_lo = 0;
+      }
       float m = -INFINITY, l = 0.f;
       RowStats rs = {0u, 0u, 0u, 0u};
       for (int j = un.kt0; j < un.kt1; ++j, ++g) {
@@ -686,15 +758,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tS + ch * 32, sr[ch]);
         ptx::tmem_wait_ld();
-        const int64_t kbase = int64_t(j) * kBN;
+        const int64_t kbase = int64_t(tile_at<kWindow>(un, j)) * kBN;
         const int lim = kbase + kBN > my_limit ? int(my_limit - kbase) : kBN;
         // partial tile for some row of the warp: hide keys at or past each
         // row's limit (the keys of a row's mask are a prefix)
-        const bool masked = __any_sync(0xffffffffu, lim < kBN);
+        bool masked = __any_sync(0xffffffffu, lim < kBN);
+        bool hidden = false;   // windowed: no row of the warp sees a key of the tile
+        int lo = 0, sink = 0;  // windowed: within the tile, [0, sink) and [lo, lim) are visible
+        if constexpr (kWindow) {
+          lo = min(max(my_lo - int(kbase), 0), kBN);
+          sink = min(max(my_sink - int(kbase), 0), kBN);
+          if (sink >= lo) lo = 0;
+          masked = __any_sync(0xffffffffu, lim < kBN || lo > 0);
+          hidden = masked && __all_sync(0xffffffffu, lim <= 0 || (lo >= lim && sink <= 0));
+        }
         const float m_old = m;
         float m_new, tile_sum;
         bool need;
-        if (j > un.kt0 && !masked) {
+        if (kWindow && hidden) {
+          // weights of zero, with neither maximum nor exponentials
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) ptx::tmem_st16(tS + ch * 16, zero);
+          m_new = m;
+          tile_sum = 0.f;
+          need = false;
+        } else if (j > un.kt0 && !masked) {
           if constexpr (kDebug) row_stats_tile(sr, uint32_t(kbase), rs);
           // speculative: exponentials against the running max while the
           // tile max is found; redone (rarely) when the max has to move
@@ -713,6 +802,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (ch * 32 + i >= lim) sr[ch][i] = 0xFF800000u;   // -inf
+            if constexpr (kWindow) {
+              if (__any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (ch * 32 + i < lo && ch * 32 + i >= sink) sr[ch][i] = 0xFF800000u;
+              }
+            }
           }
           if constexpr (kDebug) row_stats_tile(sr, uint32_t(kbase), rs);
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -818,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const uint32_t qready = lbar(B_QREADY);
     uint32_t it = 0, ul = 0;
     for (int k = 0; k < n_items; ++k, ++ul) {
-      const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+      const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
       const SeqDev& s = p.seq[un.si];
       // Every RoPE warp reaches the named barrier below, whether its own wait
       // succeeded or not, and the barrier's AND takes the stop decision for
@@ -850,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           // this CTA's 64 keys of the tile: two threads per key row, warps
           // 8-9 take chunks 0-7 (first 64 columns), warps 10-11 chunks 8-15
           const int r = rt & 63;
-          const int row = j * kBN + int(rank) * kKRows + r;
+          const int row = tile_at<kWindow>(un, j) * kBN + int(rank) * kKRows + r;
           if (row < s.Lk) {
             int pt, ph, pw;
             row_positions(p, row, s.k_t0, pt, ph, pw);
@@ -887,8 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0, ul = 0;
       bool ok = true;
       for (int k = 0; k < n_items; ++k, ++ul) {
-        const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
         const SeqDev& s = p.seq[un.si];
+        const int kv_head = kWindow ? un.head / p.group : un.head;
         if (!wait_phase(c, bar(c, B_QFREE), (ul & 1u) ^ 1u, 6)) { ok = false; break; }
         if constexpr (kDebug) {
           dev_check(p, un.head >= 0 && un.head < p.H && un.qb >= 0 && int64_t(un.qb) * kUnitRows < s.Lq, 43);
@@ -905,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           ptx::mbar_expect_tx(bar(c, B_KFULL + st), kKStageBytes);
           for (int h2 = 0; h2 < 2; ++h2)
             ptx::tma_load_3d(sK + st * kKStageBytes + h2 * kKHalfBytes, &s.tk, bar(c, B_KFULL + st), h2 * 64,
-                             un.head, j * kBN + int(rank) * kKRows);
+                             kv_head, tile_at<kWindow>(un, j) * kBN + int(rank) * kKRows);
         }
         if (!ok) { ++ul; break; }
       }
@@ -917,23 +1016,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k) {
-        const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
         const SeqDev& s = p.seq[un.si];
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
           if (!wait_phase(c, bar(c, B_VFREE + st), (n & 1u) ^ 1u, 8)) { ok = false; break; }
           ptx::mbar_expect_tx(bar(c, B_VFULL + st), kVStageBytes);
-          ptx::tma_load_3d(sV + st * kVStageBytes, &s.tv, bar(c, B_VFULL + st), int(rank) * 64, un.head, j * kBN);
+          ptx::tma_load_3d(sV + st * kVStageBytes, &s.tv, bar(c, B_VFULL + st), int(rank) * 64,
+                           kWindow ? un.head / p.group : un.head, tile_at<kWindow>(un, j) * kBN);
         }
       }
       // stopped early: let this thread's last V loads land
       if (!ok) drain_loads(bar(c, B_VFULL), it, kStages, 0u, 0u, p.timeout_ns);
-    } else if (warp == 15 && lane == 0) {
+    } else if (kWindow && warp == 15) {
+      // ===================== V landed, unseen rows cleared -> tell the leader =====================
+      // Rows of an edge tile that no row of the unit sees have weights of
+      // zero, and zero times an infinity or a NaN would enter every sum: they
+      // are overwritten with zeros (a row is 128 contiguous bytes, swizzled
+      // only within itself).
+      uint32_t it = 0;
+      bool ok = true;
+      for (int k = 0; ok && k < n_items; ++k) {
+        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        for (int j = un.kt0; j < un.kt1; ++j, ++it) {
+          const uint32_t st = it % kStages, n = it / kStages;
+          if (!wait_warp(c, bar(c, B_VFULL + st), n & 1u, 17)) { ok = false; break; }
+          const int base = tile_at<kWindow>(un, j) * kBN;
+          if (!((base + kBN <= un.hi && base >= un.lo) || base + kBN <= un.sink)) {
+            for (int x = lane; x < kBN * 8; x += 32) {
+              const int key = base + (x >> 3);
+              if (!(key < un.hi && key >= un.lo) && key >= un.sink)
+                ptx::sts128(sV + st * kVStageBytes + uint32_t(x) * 16u, make_uint4(0u, 0u, 0u, 0u));
+            }
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(lbar(B_VREADY + st));
+        }
+      }
+    } else if (!kWindow && warp == 15 && lane == 0) {
       // ===================== V landed -> tell the leader =====================
       uint32_t it = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k) {
-        const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
           if (!wait_phase(c, bar(c, B_VFULL + st), n & 1u, 17)) { ok = false; break; }
@@ -956,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0, g = 0, ul = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k, ++ul) {
-        const Unit un = decode_unit(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
         if (!wait_phase_cluster(c, bar(c, B_QREADY), ul & 1u, 9)) { ok = false; break; }
         const int nk = un.kt1 - un.kt0;   // tiles of this item; j counts them from 0
         for (int j = 0; j < nk; ++j, ++it, ++g) {
@@ -1141,15 +1267,21 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
 // Kernel instantiation: the pages' 22/21/21 split gets a compile-time axis
 // map (either pair layout); other splits read it from the parameters.  Debug
 // launches (adjacent pairs only) use the kDebug instantiations.
-static void (*attn_kernel_for(bool default_split, bool half, bool debug))(Params) {
-  if (debug) return default_split ? attn_fwd_kernel<22, 21, false, true> : attn_fwd_kernel<0, 0, false, true>;
-  if (half) return default_split ? attn_fwd_kernel<22, 21, true, false> : attn_fwd_kernel<0, 0, true, false>;
-  return default_split ? attn_fwd_kernel<22, 21, false, false> : attn_fwd_kernel<0, 0, false, false>;
+struct KernelKind {
+  bool default_split, half, debug, windowed;
+};
+static void (*attn_kernel_for(const KernelKind& k))(Params) {
+  const bool d = k.default_split;
+  if (k.windowed && k.half) return attn_fwd_kernel<0, 0, true, false, true>;
+  if (k.windowed) return d ? attn_fwd_kernel<22, 21, false, false, true> : attn_fwd_kernel<0, 0, false, false, true>;
+  if (k.debug) return d ? attn_fwd_kernel<22, 21, false, true, false> : attn_fwd_kernel<0, 0, false, true, false>;
+  if (k.half) return d ? attn_fwd_kernel<22, 21, true, false, false> : attn_fwd_kernel<0, 0, true, false, false>;
+  return d ? attn_fwd_kernel<22, 21, false, false, false> : attn_fwd_kernel<0, 0, false, false, false>;
 }
 
-static rkv_status attn_launch_shape(bool default_split, bool half, bool debug, cudaLaunchConfig_t& cfg,
-                                    cudaLaunchAttribute* attr, const void*& kern_ptr, int& max_clusters) {
-  auto kern = attn_kernel_for(default_split, half, debug);
+static rkv_status attn_launch_shape(const KernelKind& kind, cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
+                                    const void*& kern_ptr, int& max_clusters) {
+  auto kern = attn_kernel_for(kind);
   kern_ptr = reinterpret_cast<const void*>(kern);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_fwd_kernel)");
@@ -1192,7 +1324,7 @@ static bool build_schedule(Params& p, int64_t units, int max_clusters) {
   std::vector<int> cost(n);
   bool same = true;
   for (int u = 0; u < int(units); ++u) {
-    cost[size_t(u)] = decode_unit(p, u).nkt + kUnitOverheadTiles;
+    cost[size_t(u)] = host_unit(p, u).nkt + kUnitOverheadTiles;
     same = same && cost[size_t(u)] == cost[0];
   }
   if (same) return false;
@@ -1239,7 +1371,7 @@ extern "C" size_t attn_fwd_varlen_workspace_size(const rkv_attn_seq*, int32_t, i
   cudaLaunchAttribute attr[1];
   const void* kern = nullptr;
   int clusters = 0;
-  if (attn_launch_shape(true, false, false, cfg, attr, kern, clusters) != RKV_OK) {
+  if (attn_launch_shape({true, false, false, false}, cfg, attr, kern, clusters) != RKV_OK) {
     clear_error();
     return kWorkspaceBytes;
   }
@@ -1247,14 +1379,14 @@ extern "C" size_t attn_fwd_varlen_workspace_size(const rkv_attn_seq*, int32_t, i
   return kWorkspaceBytes + size_t(2 * split) * kPartBytesPerItem;
 }
 
-static rkv_status validate_seq(const rkv_attn_seq& s, int i, int32_t H) {
-  const int64_t row = int64_t(H) * kHD;
+static rkv_status validate_seq(const rkv_attn_seq& s, int i, int32_t H, int32_t H_kv) {
   if (!s.q || !s.k || !s.v || !s.o) return fail(RKV_ERR_INVALID_ARG, "seq %d: NULL tensor pointer", i);
   if (!aligned16(s.q) || !aligned16(s.k) || !aligned16(s.v) || !aligned16(s.o))
     return fail(RKV_ERR_INVALID_ARG, "seq %d: tensors must be 16-byte aligned", i);
   if (s.Lq < 1 || s.Lk < 1) return fail(RKV_ERR_INVALID_ARG, "seq %d: Lq and Lk must be >= 1", i);
   const int64_t st[4] = {s.q_stride, s.k_stride, s.v_stride, s.o_stride};
   for (int j = 0; j < 4; ++j) {
+    const int64_t row = int64_t(j == 1 || j == 2 ? H_kv : H) * kHD;
     if (st[j] < row) return fail(RKV_ERR_INVALID_ARG, "seq %d: row stride < H*D", i);
     if ((st[j] * 2) % 16) return fail(RKV_ERR_INVALID_ARG, "seq %d: rows must be 16-byte aligned", i);
     if (st[j] * 2 >= (int64_t(1) << 40)) return fail(RKV_ERR_INVALID_ARG, "seq %d: row stride too large", i);
@@ -1271,8 +1403,8 @@ static rkv_status validate_seq(const rkv_attn_seq& s, int i, int32_t H) {
 // come last, which helps the static schedule) and each one's fields that
 // number and size its work units; returns the number of units.  Fills p.F,
 // p.n_seqs, p.H and p.n_whole (= all units, before any tail split).
-static int64_t plan_units(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H, int64_t F, Params& p,
-                          int* order) {
+static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
+                          int64_t F, Params& p, int* order) {
   for (int i = 0; i < n_seqs; ++i) order[i] = i;
   for (int i = 1; i < n_seqs; ++i)
     for (int j = i; j > 0 && seqs[order[j]].Lk > seqs[order[j - 1]].Lk; --j) std::swap(order[j], order[j - 1]);
@@ -1285,6 +1417,10 @@ static int64_t plan_units(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H, i
     d.stats_row0 = row0[order[oi]];
     d.Lq = s.Lq; d.Lk = s.Lk; d.q_t0 = s.q_t0; d.k_t0 = s.k_t0;
     d.q_frame_offset = s.q_frame_offset; d.block_frames = s.block_frames; d.flags = s.flags;
+    if (windows) {
+      d.window_blocks = windows[order[oi]].window_blocks;
+      d.sink_blocks = windows[order[oi]].sink_blocks;
+    }
     d.n_qblocks = (s.Lq + kUnitRows - 1) / kUnitRows;   // 512-row blocks, one per CTA pair
     d.unit_begin = int32_t(units);
     units += int64_t(d.n_qblocks) * H;
@@ -1292,15 +1428,27 @@ static int64_t plan_units(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H, i
   p.F = uint32_t(F);
   p.n_seqs = n_seqs;
   p.H = H;
+  p.windowed = windows != nullptr;
   p.n_whole = int32_t(units < INT32_MAX ? units : INT32_MAX);
   return units;
 }
 
+// The masks of a windowed launch.
+static rkv_status validate_windows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs) {
+  for (int i = 0; i < n_seqs; ++i) {
+    if (seqs[i].block_frames < 1) return fail(RKV_ERR_INVALID_ARG, "seq %d: block_frames must be >= 1 with a window", i);
+    if (windows[i].window_blocks < 0 || windows[i].sink_blocks < 0)
+      return fail(RKV_ERR_INVALID_ARG, "seq %d: window_blocks and sink_blocks must be >= 0", i);
+  }
+  return RKV_OK;
+}
+
 // Checks, plans and launches one attention call (dbg = null for the
-// production entry points).
-static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H, int32_t D, float softmax_scale,
-                              const rkv_rope3d* rope, void* workspace, size_t workspace_bytes,
-                              const rkv_attn_debug* dbg, void* stream) {
+// production entry points; windows = null and H_kv = H except for
+// attn_fwd_window).
+static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
+                              int32_t H_kv, int32_t D, float softmax_scale, const rkv_rope3d* rope, void* workspace,
+                              size_t workspace_bytes, const rkv_attn_debug* dbg, void* stream) {
   if (!seqs || n_seqs < 1) return fail(RKV_ERR_INVALID_ARG, "need at least one sequence");
   if (n_seqs > RKV_MAX_SEQS) return fail(RKV_ERR_UNSUPPORTED, "at most %d sequences per launch", RKV_MAX_SEQS);
   if (H < 1) return fail(RKV_ERR_INVALID_ARG, "H must be >= 1");
@@ -1310,20 +1458,22 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
   if (st != RKV_OK) return st;
   if (!workspace || workspace_bytes < kWorkspaceBytes || !aligned16(workspace))
     return fail(RKV_ERR_INVALID_ARG, "workspace must be >= %zu bytes and 16-byte aligned", kWorkspaceBytes);
+  if (H_kv < 1 || H % H_kv) return fail(RKV_ERR_INVALID_ARG, "H %d must be a multiple of H_kv %d", H, H_kv);
   for (int i = 0; i < n_seqs; ++i) {
-    st = validate_seq(seqs[i], i, H);
+    st = validate_seq(seqs[i], i, H, H_kv);
     if (st != RKV_OK) return st;
   }
+  if (windows && (st = validate_windows(seqs, windows, n_seqs)) != RKV_OK) return st;
   // outputs may not share a byte with any input or other output; row-strided
   // views of one tensor with disjoint heads (a launch over head slices) pass
-  const int64_t row_bytes = int64_t(H) * kHD * 2;
+  const int64_t row_bytes = int64_t(H) * kHD * 2, kv_bytes = int64_t(H_kv) * kHD * 2;
   for (int i = 0; i < n_seqs; ++i) {
     const rkv_attn_seq& s = seqs[i];
     for (int j = 0; j < n_seqs; ++j) {
       const rkv_attn_seq& t = seqs[j];
       if (rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.q, t.Lq, t.q_stride * 2, row_bytes) ||
-          rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.k, t.Lk, t.k_stride * 2, row_bytes) ||
-          rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.v, t.Lk, t.v_stride * 2, row_bytes) ||
+          rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.k, t.Lk, t.k_stride * 2, kv_bytes) ||
+          rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.v, t.Lk, t.v_stride * 2, kv_bytes) ||
           (i != j && rows_overlap(s.o, s.Lq, s.o_stride * 2, row_bytes, t.o, t.Lq, t.o_stride * 2, row_bytes)))
         return fail(RKV_ERR_INVALID_ARG, "seq %d: output overlaps an input or another output", i);
     }
@@ -1333,15 +1483,16 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
   memset(&p, 0, sizeof(p));
   const int64_t F = int64_t(rope->grid_h) * rope->grid_w;
   int order[RKV_MAX_SEQS];
-  const int64_t units = plan_units(seqs, n_seqs, H, F, p, order);
+  const int64_t units = plan_units(seqs, windows, n_seqs, H, F, p, order);
+  p.group = H / H_kv;
 
   int64_t t_lo = INT64_MAX, t_hi = INT64_MIN;
   for (int oi = 0; oi < n_seqs; ++oi) {
     const rkv_attn_seq& s = seqs[order[oi]];
     SeqDev& d = p.seq[oi];
     if ((st = make_map(&d.tq, s.q, s.Lq, H, s.q_stride, kBM)) != RKV_OK) return st;
-    if ((st = make_map(&d.tk, s.k, s.Lk, H, s.k_stride, kKRows)) != RKV_OK) return st;
-    if ((st = make_map(&d.tv, s.v, s.Lk, H, s.v_stride, kBN)) != RKV_OK) return st;
+    if ((st = make_map(&d.tk, s.k, s.Lk, H_kv, s.k_stride, kKRows)) != RKV_OK) return st;
+    if ((st = make_map(&d.tv, s.v, s.Lk, H_kv, s.v_stride, kBN)) != RKV_OK) return st;
     d.o = static_cast<uint8_t*>(s.o);
     d.o_stride_bytes = s.o_stride * 2;
     if (s.flags & RKV_ROPE_Q) {
@@ -1359,7 +1510,9 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
   const int32_t pairs[3] = {rope->pairs_t, rope->pairs_h, rope->pairs_w};
   for (int a = 0; a < 3; ++a)
     if (pairs[a] < 4) return fail(RKV_ERR_UNSUPPORTED, "fused RoPE needs >= 4 rotary pairs per axis");
-  const int64_t npos[3] = {n_t, rope->grid_h, rope->grid_w};
+  // a windowed launch that rotates nothing needs no table (its frame grid may be any size)
+  const bool no_table = windows && n_t <= 0;
+  const int64_t npos[3] = {n_t, no_table ? 1 : rope->grid_h, no_table ? 1 : rope->grid_w};
   int64_t entries = 0;
   int32_t first = 0;
   for (int a = 0; a < 3; ++a) {
@@ -1410,9 +1563,8 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
   cudaLaunchAttribute attr[1];
   const void* kern = nullptr;
   int max_clusters = 0;
-  const bool half = rope->layout == RKV_ROPE_HALF;
-  if ((st = attn_launch_shape(default_split, half, dbg != nullptr, cfg, attr, kern, max_clusters)) != RKV_OK)
-    return st;
+  const KernelKind kind = {default_split, rope->layout == RKV_ROPE_HALF, dbg != nullptr, windows != nullptr};
+  if ((st = attn_launch_shape(kind, cfg, attr, kern, max_clusters)) != RKV_OK) return st;
   cfg.stream = cs;
 
   // Units of different cost (frame-block-masked sequences, or sequences of
@@ -1435,10 +1587,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
     const int head = int(local / d.n_qblocks);
     const int ord = int(local - int64_t(head) * d.n_qblocks);
     const int qb = d.block_frames > 0 ? (d.n_qblocks - 1 - ord) : ord;
-    int64_t last = int64_t(qb + 1) * kUnitRows - 1;
-    if (last > d.Lq - 1) last = d.Lq - 1;
-    const int64_t kv = row_kv_limit(d, p, int(last));
-    if ((kv + kBN - 1) / kBN < 2) { n_split = 0; break; }
+    if (host_unit(p, int(u)).nkt < 2) { n_split = 0; break; }
     ca.unit[k].o = d.o;
     ca.unit[k].o_stride_bytes = d.o_stride_bytes;
     ca.unit[k].Lq = d.Lq;
@@ -1464,7 +1613,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t 
   }
   // one CTA pair per pair of SMs that can hold it (persistent)
   cfg.gridDim = dim3(uint32_t(2 * std::min<int64_t>(p.total_units, max_clusters)));
-  e = cudaLaunchKernelEx(&cfg, attn_kernel_for(default_split, half, dbg != nullptr), p);
+  e = cudaLaunchKernelEx(&cfg, attn_kernel_for(kind), p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_kernel launch");
   if (n_split > 0) {
@@ -1481,7 +1630,17 @@ extern "C" rkv_status attn_fwd_varlen(const rkv_attn_seq* seqs, int32_t n_seqs, 
                                       size_t workspace_bytes, void* stream) {
   NvtxRange nvtx_range("attn_fwd_varlen");
   clear_error();
-  return attn_launch(seqs, n_seqs, H, D, softmax_scale, rope, workspace, workspace_bytes, nullptr, stream);
+  return attn_launch(seqs, nullptr, n_seqs, H, H, D, softmax_scale, rope, workspace, workspace_bytes, nullptr, stream);
+}
+
+extern "C" rkv_status attn_fwd_window(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs,
+                                      int32_t H, int32_t H_kv, int32_t D, float softmax_scale, const rkv_rope3d* rope,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("attn_fwd_window");
+  clear_error();
+  if (!windows) return fail(RKV_ERR_INVALID_ARG, "windows is NULL");
+  return attn_launch(seqs, windows, n_seqs, H, H_kv, D, softmax_scale, rope, workspace, workspace_bytes, nullptr,
+                     stream);
 }
 
 extern "C" rkv_status attn_fwd_varlen_debug(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H, int32_t D,
@@ -1494,14 +1653,14 @@ extern "C" rkv_status attn_fwd_varlen_debug(const rkv_attn_seq* seqs, int32_t n_
   if (dbg->row_stats && !aligned16(dbg->row_stats)) return fail(RKV_ERR_INVALID_ARG, "row_stats must be 16-byte aligned");
   if (rope && rope->layout != RKV_ROPE_ADJACENT)
     return fail(RKV_ERR_UNSUPPORTED, "debug launches support the adjacent RoPE pair layout only");
-  return attn_launch(seqs, n_seqs, H, D, softmax_scale, rope, workspace, workspace_bytes, dbg, stream);
+  return attn_launch(seqs, nullptr, n_seqs, H, H, D, softmax_scale, rope, workspace, workspace_bytes, dbg, stream);
 }
 
-extern "C" rkv_status rkv_attn_mask_rows(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H,
-                                         const rkv_rope3d* rope, int64_t* row_limit, int32_t* unit_tiles,
-                                         int64_t* n_units) {
-  NvtxRange nvtx_range("rkv_attn_mask_rows");
-  clear_error();
+// The mask and unit plan on the host, for rkv_attn_mask_rows (windows and the
+// sink / begin arrays null) and rkv_attn_window_rows.
+static rkv_status host_mask(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
+                            const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
+                            int32_t* unit_tiles, int64_t* n_units) {
   if (!seqs || n_seqs < 1) return fail(RKV_ERR_INVALID_ARG, "need at least one sequence");
   if (n_seqs > RKV_MAX_SEQS) return fail(RKV_ERR_UNSUPPORTED, "at most %d sequences per launch", RKV_MAX_SEQS);
   if (H < 1) return fail(RKV_ERR_INVALID_ARG, "H must be >= 1");
@@ -1515,21 +1674,28 @@ extern "C" rkv_status rkv_attn_mask_rows(const rkv_attn_seq* seqs, int32_t n_seq
     if (s.block_frames > 0 && s.q_frame_offset < 0)
       return fail(RKV_ERR_INVALID_ARG, "seq %d: q_frame_offset must be >= 0 with a mask", i);
   }
+  if (windows && (st = validate_windows(seqs, windows, n_seqs)) != RKV_OK) return st;
   Params p;
   memset(&p, 0, sizeof(p));
   int order[RKV_MAX_SEQS], where[RKV_MAX_SEQS];
-  const int64_t units = plan_units(seqs, n_seqs, H, int64_t(rope->grid_h) * rope->grid_w, p, order);
+  const int64_t units = plan_units(seqs, windows, n_seqs, H, int64_t(rope->grid_h) * rope->grid_w, p, order);
   if (units >= (int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   for (int oi = 0; oi < n_seqs; ++oi) where[order[oi]] = oi;
   int64_t off = 0;
   for (int i = 0; i < n_seqs; ++i) {
     const SeqDev& d = p.seq[where[i]];
-    for (int r = 0; r < d.Lq; ++r) row_limit[off + r] = row_kv_limit(d, p, r);
+    for (int r = 0; r < d.Lq; ++r) {
+      row_limit[off + r] = row_kv_limit(d, p, r);
+      if (windows) {
+        row_sink[off + r] = row_kv_sink(d, p, r);
+        row_begin[off + r] = row_kv_begin(d, p, r);
+      }
+    }
     off += d.Lq;
   }
   if (unit_tiles) {
     for (int64_t u = 0; u < units; ++u) {
-      const Unit un = decode_unit(p, int(u));
+      const Unit un = host_unit(p, int(u));
       unit_tiles[4 * u + 0] = order[un.si];
       unit_tiles[4 * u + 1] = un.head;
       unit_tiles[4 * u + 2] = un.qb;
@@ -1538,6 +1704,24 @@ extern "C" rkv_status rkv_attn_mask_rows(const rkv_attn_seq* seqs, int32_t n_seq
   }
   if (n_units) *n_units = units;
   return RKV_OK;
+}
+
+extern "C" rkv_status rkv_attn_mask_rows(const rkv_attn_seq* seqs, int32_t n_seqs, int32_t H,
+                                         const rkv_rope3d* rope, int64_t* row_limit, int32_t* unit_tiles,
+                                         int64_t* n_units) {
+  NvtxRange nvtx_range("rkv_attn_mask_rows");
+  clear_error();
+  return host_mask(seqs, nullptr, n_seqs, H, rope, nullptr, nullptr, row_limit, unit_tiles, n_units);
+}
+
+extern "C" rkv_status rkv_attn_window_rows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs,
+                                           int32_t H, const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin,
+                                           int64_t* row_limit, int32_t* unit_tiles, int64_t* n_units) {
+  NvtxRange nvtx_range("rkv_attn_window_rows");
+  clear_error();
+  if (!windows) return fail(RKV_ERR_INVALID_ARG, "windows is NULL");
+  if (!row_sink || !row_begin) return fail(RKV_ERR_INVALID_ARG, "row_sink/row_begin is NULL");
+  return host_mask(seqs, windows, n_seqs, H, rope, row_sink, row_begin, row_limit, unit_tiles, n_units);
 }
 
 extern "C" rkv_status rkv_attn_status(void* workspace, void* stream) {
@@ -1612,7 +1796,7 @@ extern "C" rkv_status attn_fwd_varlen_noalloc(const rkv_attn_seq* seqs, int32_t 
   void* ws = nullptr;
   rkv_status st = noalloc_scratch(&ws);
   if (st != RKV_OK) return st;
-  return attn_launch(seqs, n_seqs, H, D, softmax_scale, rope, ws, kNoAllocScratchBytes, nullptr, stream);
+  return attn_launch(seqs, nullptr, n_seqs, H, H, D, softmax_scale, rope, ws, kNoAllocScratchBytes, nullptr, stream);
 }
 
 extern "C" rkv_status rkv_attn_noalloc_status(void* stream) {

@@ -1,0 +1,66 @@
+// What the paged-cache kernels share: the cache as a kernel sees it, the
+// checks a kernel makes because lengths and page tables live on the device,
+// and the host checks of an rkv_paged_cache.
+#pragma once
+
+#include "common.cuh"
+
+namespace rkv {
+namespace paged {
+
+constexpr int kHD = 128;                  // head dim
+constexpr uint32_t kRowBytes = kHD * 2;   // one token of one key head: the unit rows are counted in
+
+struct CacheDev {
+  uint8_t* k;
+  uint8_t* v;
+  const int32_t* table;
+  int64_t table_stride;
+  int32_t* status;
+  uint32_t page_units;   // head rows (of kRowBytes) between pages
+  uint32_t n_pages;
+  uint32_t P;            // tokens per page
+  FastDiv div_P;
+  int32_t H, n_seqs, capacity;
+};
+
+// Where a device-side finding was made (status word: RKV_ERR_DEVICE_CHECK in
+// the low byte, this above it).
+enum : int { kBadLength = 1, kBadPage = 2 };
+
+__device__ __forceinline__ void record(const CacheDev& c, int what) {
+  if (c.status) atomicCAS(c.status, 0, int(RKV_ERR_DEVICE_CHECK) | (what << 8));
+}
+
+// Length of sequence s, brought into [0, capacity].
+__device__ __forceinline__ int seq_len(const CacheDev& c, const int32_t* seq_lens, int s) {
+  const int L = seq_lens[s];
+  if (L < 0 || L > c.capacity) {
+    record(c, kBadLength);
+    return L < 0 ? 0 : c.capacity;
+  }
+  return L;
+}
+
+// Page of token j of sequence s (j < capacity), and the head row of (page,
+// token, head h) counted from the start of the pool (below 2^32, checked on
+// the host).
+__device__ __forceinline__ uint32_t page_of(const CacheDev& c, int s, uint32_t j) {
+  return uint32_t(c.table[int64_t(s) * c.table_stride + fdiv(j, c.div_P)]);
+}
+__device__ __forceinline__ uint32_t row_unit(const CacheDev& c, uint32_t page, uint32_t j, int h) {
+  const uint32_t tok = j - fdiv(j, c.div_P) * c.P;
+  return page * c.page_units + tok * uint32_t(c.H) + uint32_t(h);
+}
+
+// ---- host -------------------------------------------------------------------------
+rkv_status check_cache(const rkv_paged_cache* c);
+CacheDev cache_dev(const rkv_paged_cache* c);   // of a checked cache
+// Does [p, p + bytes) share a byte with a page of the pool?
+bool overlaps_pool(const rkv_paged_cache* c, const void* p, uint64_t bytes);
+int sm_count();
+
+inline int64_t capacity(const rkv_paged_cache* c) { return int64_t(c->max_pages) * c->page_tokens; }
+
+}  // namespace paged
+}  // namespace rkv

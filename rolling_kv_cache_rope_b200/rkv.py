@@ -63,6 +63,20 @@ RKV_DEBUG_STALL_NONE, RKV_DEBUG_STALL_V_READY, RKV_DEBUG_STALL_K_READY, RKV_DEBU
 RKV_DEBUG_STALL_BULK_LOAD = 1
 
 
+class rkv_attn_window(ctypes.Structure):
+    _fields_ = [("window_blocks", ctypes.c_int32), ("sink_blocks", ctypes.c_int32)]
+
+
+class rkv_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("status", ctypes.c_void_p)]
+
+
+RKV_DECODE_MAX_LQ = 64
+
+
 class rkv_ring(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("slots", ctypes.c_int32),
                 ("tokens_per_frame", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32),
@@ -104,6 +118,31 @@ _lib.kvcache_ring_update_rope.argtypes = [_c.POINTER(rkv_ring), _c.c_void_p, _c.
 _lib.kvcache_ring_update_debug.restype = _c.c_int
 _lib.kvcache_ring_update_debug.argtypes = [_c.POINTER(rkv_ring), _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int32,
                                            _c.POINTER(_c.c_int32), _c.POINTER(rkv_ring_debug), _c.c_void_p]
+_lib.attn_fwd_window.restype = _c.c_int
+_lib.attn_fwd_window.argtypes = [_c.POINTER(rkv_attn_seq), _c.POINTER(rkv_attn_window), _c.c_int32, _c.c_int32,
+                                 _c.c_int32, _c.c_int32, _c.c_float, _c.POINTER(rkv_rope3d), _c.c_void_p, _c.c_size_t,
+                                 _c.c_void_p]
+_lib.rkv_attn_window_rows.restype = _c.c_int
+_lib.rkv_attn_window_rows.argtypes = [_c.POINTER(rkv_attn_seq), _c.POINTER(rkv_attn_window), _c.c_int32, _c.c_int32,
+                                      _c.POINTER(rkv_rope3d), _c.POINTER(_c.c_int64), _c.POINTER(_c.c_int64),
+                                      _c.POINTER(_c.c_int64), _c.POINTER(_c.c_int32), _c.POINTER(_c.c_int64)]
+_lib.kvcache_paged_insert.restype = _c.c_int
+_lib.kvcache_paged_insert.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int32,
+                                      _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p]
+_lib.attn_decode_paged_workspace_size.restype = _c.c_size_t
+_lib.attn_decode_paged_workspace_size.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_int32, _c.c_int32, _c.c_int32]
+_lib.attn_decode_paged.restype = _c.c_int
+_lib.attn_decode_paged.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
+                                   _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_float, _c.c_int32, _c.c_int32,
+                                   _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]
+_lib.kvcache_paged_evict_workspace_size.restype = _c.c_size_t
+_lib.kvcache_paged_evict_workspace_size.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_int32]
+_lib.kvcache_paged_evict.restype = _c.c_int
+_lib.kvcache_paged_evict.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                     _c.c_int32, _c.c_int32, _c.c_int32, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                     _c.c_void_p, _c.c_size_t, _c.c_void_p]
+_lib.rkv_paged_status.restype = _c.c_int
+_lib.rkv_paged_status.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_void_p]
 _lib.rkv_ring_status.restype = _c.c_int
 _lib.rkv_ring_status.argtypes = [_c.c_void_p]
 _lib.rkv_ring_slot.restype = _c.c_int32
@@ -436,3 +475,234 @@ def kvcache_ring_update_rope(ring, k_new, v_new, t0, rope, n_frames=None, stream
     _check(_lib.kvcache_ring_update_rope(ctypes.byref(ring.c), k_new.data_ptr(), v_new.data_ptr(), ks, n_frames,
                                          int(t0), ctypes.byref(rope), ctypes.byref(ev), _stream(stream)))
     return ev.value
+
+
+def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, stream=None):
+    """Run every AttnSeq (block_frames >= 1 each) in one launch with a sliding
+    window and first blocks that stay visible; ``windows``: one
+    (window_blocks, sink_blocks) per sequence, window_blocks = 0 for none.
+    k and v may have fewer heads than q (grouped heads).  Returns the
+    workspace (attn_fwd_varlen_workspace_size() bytes, allocated here when
+    None; rkv_attn_status reads it)."""
+    import torch
+    if not seqs:
+        raise ValueError("need at least one sequence")
+    if len(windows) != len(seqs):
+        raise ValueError("need one (window_blocks, sink_blocks) per sequence")
+    H, D, H_kv = seqs[0].q.shape[1], seqs[0].q.shape[2], seqs[0].k.shape[1]
+    for s in seqs:
+        if tuple(s.q.shape[1:]) != (H, D) or tuple(s.o.shape[1:]) != (H, D) or tuple(s.k.shape[1:]) != (H_kv, D) \
+                or tuple(s.v.shape[1:]) != (H_kv, D):
+            raise ValueError("the sequences of one launch share the numbers of query and key heads")
+    arr = (rkv_attn_seq * len(seqs))(*[s.to_c() for s in seqs])
+    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(int(w), int(k)) for w, k in windows])
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    with _on(seqs[0].q, stream) as st:
+        if workspace is None:
+            workspace = torch.empty(attn_fwd_varlen_workspace_size(len(seqs), H, D), dtype=torch.uint8,
+                                    device=seqs[0].q.device)
+        _check(_lib.attn_fwd_window(arr, win, len(seqs), H, H_kv, D, float(softmax_scale), ctypes.byref(rope),
+                                    workspace.data_ptr(), workspace.numel(), st))
+    return workspace
+
+
+def attn_window_rows(seqs, windows, H, rope):
+    """The mask and key-tile plan attn_fwd_window uses, evaluated on the host
+    by the kernel's own code (no GPU needed).  ``seqs``: dicts with Lq, Lk,
+    block_frames and optional q_frame_offset.  Returns (sink, begin, limit,
+    units): lists per sequence of per-row key ranges [0, sink) and [begin,
+    limit), and units as attn_mask_rows gives them."""
+    import numpy as np
+    arr = (rkv_attn_seq * len(seqs))(*[
+        rkv_attn_seq(Lq=int(s["Lq"]), Lk=int(s["Lk"]), q_frame_offset=int(s.get("q_frame_offset", 0)),
+                     block_frames=int(s["block_frames"])) for s in seqs])
+    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(int(w), int(k)) for w, k in windows])
+    lq = [int(s["Lq"]) for s in seqs]
+    got = [np.zeros(max(1, sum(lq)), dtype=np.int64) for _ in range(3)]
+    units = np.zeros((max(1, sum(int(H) * ((x + 511) // 512) for x in lq)), 4), dtype=np.int32)
+    n = ctypes.c_int64(0)
+    p64 = ctypes.POINTER(ctypes.c_int64)
+    _check(_lib.rkv_attn_window_rows(arr, win, len(seqs), int(H), ctypes.byref(rope),
+                                     *[g.ctypes.data_as(p64) for g in got],
+                                     units.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), ctypes.byref(n)))
+    at = np.cumsum([0] + lq)
+    return (*[[g[at[i]:at[i + 1]].copy() for i in range(len(lq))] for g in got], units[:n.value])
+
+
+class _on:
+    """Stream handle of a call on tensors of t's device: the given stream, or
+    the device's current one.  Inside, that device and stream are current, so
+    what the call allocates belongs to the stream it runs on."""
+
+    __slots__ = ("guards", "device", "stream")
+
+    def __init__(self, t, stream):
+        self.device, self.stream, self.guards = t.device, stream, []
+
+    def __enter__(self):
+        import torch
+        if self.device.type != "cuda":
+            return ctypes.c_void_p(0)   # nothing runs: the library refuses host tensors' work
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError("the stream and the tensors are on different devices")
+            g = torch.cuda.stream(self.stream)      # makes the stream's device current too
+        elif self.device.index != torch.cuda.current_device():
+            g = torch.cuda.device(self.device)
+        else:
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(self.device.index))
+        g.__enter__()
+        self.guards.append(g)
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        while self.guards:
+            self.guards.pop().__exit__(*exc)
+        return False
+
+
+class PagedKVCache:
+    """A paged cache of several token streams over caller tensors (see
+    rkv_paged_cache): ``k``, ``v`` bf16 CUDA [n_pages, page_tokens, H, 128]
+    (each page contiguous; the buffers of a KVRing are one), ``page_table``
+    int32 CUDA [n_seqs, max_pages].  ``status`` is the word device-side checks
+    record in (rkv_paged_status)."""
+
+    def __init__(self, k, v, page_table):
+        import torch
+        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 4 or not k.is_cuda or not v.is_cuda:
+            raise ValueError("k and v must be bf16 CUDA tensors of shape [n_pages, page_tokens, H, D]")
+        n_pages, P, H, D = k.shape
+        if v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("k and v must share shape, strides and device")
+        if k.stride()[1:] != (H * D, D, 1):
+            raise ValueError("a page must be contiguous")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != k.device \
+                or page_table.stride(1) != 1:
+            raise ValueError("page_table must be int32 [n_seqs, max_pages] with contiguous rows, on the device of k")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.n_seqs, self.max_pages = page_table.shape
+        self.H, self.capacity = H, self.max_pages * P
+        # a single page's or sequence's stride says nothing: any will do
+        stride = k.stride(0) if n_pages > 1 else P * H * D
+        table_stride = page_table.stride(0) if self.n_seqs > 1 else self.max_pages
+        self.c = rkv_paged_cache(k.data_ptr(), v.data_ptr(), stride, n_pages, P, H, D, page_table.data_ptr(),
+                                 table_stride, self.n_seqs, self.max_pages, self.status.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    def _ints(self, t, name):
+        """Device pointer of an int32 [n_seqs] tensor."""
+        import torch
+        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != self.n_seqs or not t.is_contiguous() \
+                or t.device != self.k.device:
+            raise ValueError(f"{name} must be a contiguous int32 [n_seqs={self.n_seqs}] tensor on the cache's device")
+        return t.data_ptr()
+
+    def _scores(self, t, name, dtype):
+        """Device pointer of a [n_seqs, H, capacity] tensor, or NULL for None."""
+        if t is None:
+            return None
+        if t.dtype != dtype or t.shape != (self.n_seqs, self.H, self.capacity) or not t.is_contiguous() \
+                or t.device != self.k.device:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                             f"{(self.n_seqs, self.H, self.capacity)} on the cache's device")
+        return t.data_ptr()
+
+    def _workspace(self, t, size):
+        import torch
+        if t is None:
+            return torch.empty(max(16, size), dtype=torch.uint8, device=self.k.device)
+        if t.device != self.k.device or not t.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        return t
+
+
+def kvcache_paged_insert(cache, k_new, v_new, seq_lens, next_pos=None, pos=None, weight=None, stream=None):
+    """Write the newest tokens of every sequence, k_new and v_new bf16
+    [n_seqs * n_new, H, 128] sequence by sequence; ``seq_lens`` (int32 CUDA
+    [n_seqs]) counts them already.  ``pos`` (with ``next_pos``) and ``weight``:
+    the scores of the new tokens (see rkv.h)."""
+    import torch
+    ks, vs = _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (cache.H, 128) or k_new.shape[0] % cache.n_seqs:
+        raise ValueError(f"k_new and v_new must be [n_seqs * n_new, {cache.H}, 128]")
+    if ks != vs:
+        raise ValueError("k_new and v_new must share a row stride")
+    if k_new.device != cache.k.device or v_new.device != cache.k.device:
+        raise ValueError("k_new and v_new must be on the cache's device")
+    n_new = k_new.shape[0] // cache.n_seqs
+    with _on(cache.k, stream) as st:
+        _check(_lib.kvcache_paged_insert(cache.ref, k_new.data_ptr(), v_new.data_ptr(), ks, n_new,
+                                         cache._ints(seq_lens, "seq_lens"),
+                                         None if next_pos is None else cache._ints(next_pos, "next_pos"),
+                                         cache._scores(pos, "pos", torch.int32),
+                                         cache._scores(weight, "weight", torch.float32), st))
+
+
+def attn_decode_paged_workspace_size(cache, Hq, Lq=1, weights=False):
+    return int(_lib.attn_decode_paged_workspace_size(cache.ref, int(Hq), int(Lq), 1 if weights else 0))
+
+
+def attn_decode_paged(q, cache, seq_lens, o=None, window=0, sinks=0, softmax_scale=None, weight_in=None,
+                      weight_out=None, workspace=None, stream=None):
+    """Attention of the newest Lq tokens of every sequence over its pages: q
+    bf16 [n_seqs * Lq, Hq, 128], sequence by sequence; ``seq_lens`` counts
+    them.  ``window`` / ``sinks``: a token sees the last ``window`` tokens and
+    the first ``sinks`` (0 = all).  ``weight_out`` = ``weight_in`` + the
+    attention weight each cached token received (may be the same tensor).
+    Returns o (allocated here when None)."""
+    import torch
+    qs = _rows(q, "q")
+    if q.shape[0] % cache.n_seqs or q.device != cache.k.device:
+        raise ValueError(f"q must be [n_seqs * Lq, Hq, 128] with n_seqs = {cache.n_seqs}, on the cache's device")
+    Lq, Hq, D = q.shape[0] // cache.n_seqs, q.shape[1], q.shape[2]
+    if D != 128:
+        raise ValueError("head_dim must be 128")
+    with _on(cache.k, stream) as st:
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        os_ = _rows(o, "o")
+        if o.shape != q.shape or o.device != q.device:
+            raise ValueError("o and q must share shape and device")
+        size = 0 if workspace is not None else attn_decode_paged_workspace_size(cache, Hq, Lq, weight_out is not None)
+        workspace = cache._workspace(workspace, size)
+        _check(_lib.attn_decode_paged(cache.ref, q.data_ptr(), o.data_ptr(), qs, os_, Hq, Lq,
+                                      cache._ints(seq_lens, "seq_lens"),
+                                      1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale),
+                                      int(window), int(sinks), cache._scores(weight_in, "weight_in", torch.float32),
+                                      cache._scores(weight_out, "weight_out", torch.float32), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), st))
+    return o
+
+
+def kvcache_paged_evict_workspace_size(cache, budget):
+    return int(_lib.kvcache_paged_evict_workspace_size(cache.ref, int(budget)))
+
+
+def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0, recent=0, seq_lens_out=None,
+                        weight_out=None, pos_out=None, workspace=None, stream=None):
+    """Cut every sequence to ``budget`` tokens per key head, dropping those of
+    the least accumulated weight (see rkv.h).  The outputs default to their
+    inputs (in place)."""
+    import torch
+    if (weight_out is None) != (pos_out is None):
+        raise ValueError("weight_out and pos_out go together")
+    with _on(cache.k, stream) as st:
+        size = 0 if workspace is not None else kvcache_paged_evict_workspace_size(cache, budget)
+        workspace = cache._workspace(workspace, size)
+        _check(_lib.kvcache_paged_evict(
+            cache.ref, cache._ints(seq_lens, "seq_lens"), cache._scores(weight, "weight", torch.float32),
+            cache._scores(pos, "pos", torch.int32), cache._ints(next_pos, "next_pos"), int(budget), int(sinks),
+            int(recent), cache._ints(seq_lens if seq_lens_out is None else seq_lens_out, "seq_lens_out"),
+            cache._scores(weight if weight_out is None else weight_out, "weight_out", torch.float32),
+            cache._scores(pos if pos_out is None else pos_out, "pos_out", torch.int32), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st))
+
+
+def rkv_paged_status(cache, stream=None):
+    """Synchronise and raise RkvError if a call on ``cache`` met a length or a
+    page out of range since the last report."""
+    with _on(cache.k, stream) as st:
+        _check(_lib.rkv_paged_status(cache.ref, st))
