@@ -19,25 +19,25 @@
 // this bandwidth (16 keys of a head cost 32 of them per 8 KB).
 //
 // Split: the key rows of all (sequence, key head, row block) items, in steps
-// of 128 keys, form one list of T steps, and block b of C takes the steps
-// [b T / C, (b + 1) T / C): every block gets the same bytes whatever the
-// lengths.  An item that lies in one block is finished there; of the others
+// of 64 keys, form one list of T steps, and each of C blocks takes T / C of
+// them in a row: every block gets the same bytes whatever the lengths.  An item that lies in one block is finished there; of the others
 // each block leaves its running maximum, sum and unnormalised O (at most two
 // per block), and a second launch joins them in the order of the keys, so the
 // result does not depend on timing.  Each kernel derives the list from
 // seq_lens itself: nothing is planned on the host, and a captured launch
 // serves growing sequences.
 //
-// Inside a block: eight warps, each with 16 of a step's 128 keys and its own
+// Inside a block: four warps, each with 16 of a step's 64 keys and its own
 // maximum, sum and O in registers, meet only where an item begins or ends.
 // Each warp copies its own K and V rows with 16-byte asynchronous copies into
-// its part of a ring of stages, so several steps (64 KB each) are in flight
+// its part of a ring of stages, so several steps (32 KB each) are in flight
 // per SM without registers holding data, across the ends of items too.  A row
 // that is not visible to any query (past the end, outside window and sinks, on
 // a bad page) is not read but zero-filled, so nothing it holds can enter a sum.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "sm100_ptx.cuh"
@@ -45,16 +45,15 @@
 namespace rkv {
 namespace paged {
 
-constexpr int kDecThreads = 256;
-constexpr int kDecWarps = kDecThreads / 32;
-constexpr int kTileKeys = 16;                          // keys of a step one warp takes
-constexpr int kStepKeys = kDecWarps * kTileKeys;       // 128
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecPerSm = 2;                           // blocks of the main launch an SM holds
+constexpr int kTileKeys = 16;                          // keys a warp takes at a time
 constexpr int kTileBytes = kTileKeys * int(kRowBytes); // 4 KB of K, as much of V
-constexpr int kStepBytes = kDecWarps * 2 * kTileBytes; // 64 KB
+constexpr int kRingBytes = 96 * 1024;                  // K and V stages of a block
 constexpr float kMaxSlack = 8.0f;                      // the running maximum moves past 2^8 growth only
 constexpr int kMaxRows = 4096;                         // query rows of a key head (Lq * G)
 constexpr int kJoinThreads = 256;
-constexpr int kWeightTokens = kJoinThreads;            // tokens of a step of the weights pass
 
 struct DecodeArgs {
   CacheDev c;
@@ -67,20 +66,33 @@ struct DecodeArgs {
   float* part_o;                 // [C][2][rows_blk][kHD]
   float2* part_ml;               // [C][2][rows_blk] running maximum (log2 units) and sum
   float2* item_ml;               // [items][rows_blk] of items finished in one block (weights only)
-  float* scores;                 // [T][rows_blk][kStepKeys] scaled scores, log2 units (weights only)
+  float* scores;                 // [T][rows_blk][step_keys] scaled scores, log2 units (weights only)
+  struct BlockRec* recs;         // [C]
   float scale_log2;
   int32_t Hq, Lq, G, rows;       // rows = Lq * G
-  int32_t rows_tile;             // rows a row block has room for (16 or 32)
+  FastDiv div_G;
+  int32_t rows_tile;             // rows a row block has room for: 16, 32 or 64
+  int32_t step_keys;             // keys of a step: 64, 32 or 16
   int32_t rows_blk, n_blk;       // rows of a full row block (min(rows, rows_tile)), row blocks
   int32_t window, sinks;
   int32_t main_blocks;           // C
+  FastDiv div_blocks;
+};
+
+// What a block of the main launch leaves for the join: the place its steps
+// began at, and the item it joins (one that began in the block and goes on in
+// others; parts = 0: none).
+struct alignas(16) BlockRec {
+  int32_t s, g, blk, c;         // first step
+  int32_t first, n, total;      // ... its number in the whole list, the block's steps, the list's length
+  int32_t join_s, join_g, join_blk, parts, slot;
 };
 
 // The keys any query of a sequence of length L sees, as a list of `span`
 // entries: [0, se), then [lo, L).
 struct Span {
   int L, se, lo, span;
-  __device__ __forceinline__ int steps() const { return (span + kStepKeys - 1) / kStepKeys; }
+  __device__ __forceinline__ int steps(int keys) const { return (span + keys - 1) / keys; }
 };
 
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int L) {
@@ -92,40 +104,26 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int L) {
   return r;
 }
 
-// Steps of a sequence in the list of visible keys (main launch), per item.
-struct MainSteps {
-  __device__ __forceinline__ static int of(const DecodeArgs& a, int s) {
-    return span_of(a, seq_len(a.c, a.seq_lens, s)).steps();
-  }
-};
-// Steps of a sequence's tokens, visible or not, in the weights pass, per key head.
-struct TokenSteps {
-  __device__ __forceinline__ static int of(const DecodeArgs& a, int s) {
-    return (seq_len(a.c, a.seq_lens, s) + kWeightTokens - 1) / kWeightTokens;
-  }
-};
-
-// Steps of the whole list: `items` times each sequence's.  Whole warps call
-// these two; every lane gets the result.
-template <class Steps>
-__device__ __forceinline__ int total_steps(const DecodeArgs& a, int items) {
-  int total = 0;
-  for (int s = threadIdx.x & 31; s < a.c.n_seqs; s += 32) total += Steps::of(a, s);
-  return __reduce_add_sync(0xffffffffu, total) * items;
+__device__ __forceinline__ int seq_steps(const DecodeArgs& a, int s) {
+  return span_of(a, seq_len(a.c, a.seq_lens, s)).steps(a.step_keys);
 }
 
-// The sequence that step x of the list falls into and the steps before it.
+// The list of steps: sequence by sequence, `items` times the steps of each.
+// Whole warps call these; every lane gets the result.
 struct Place {
-  int s, base;
+  int s, base;   // sequence a step falls into, and the steps before that sequence
 };
-
-template <class Steps>
+__device__ __forceinline__ int total_steps(const DecodeArgs& a, int items) {
+  int total = 0;
+  for (int s = threadIdx.x & 31; s < a.c.n_seqs; s += 32) total += seq_steps(a, s);
+  return __reduce_add_sync(0xffffffffu, total) * items;
+}
 __device__ __forceinline__ Place find_step(const DecodeArgs& a, int items, int x) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int b = 0; b < a.c.n_seqs; b += 32) {
     const int s = b + lane;
-    const int own = s < a.c.n_seqs ? Steps::of(a, s) * items : 0;
+    const int own = s < a.c.n_seqs ? seq_steps(a, s) * items : 0;
     int inc = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -142,38 +140,45 @@ __device__ __forceinline__ Place find_step(const DecodeArgs& a, int items, int x
   return {a.c.n_seqs, before};   // x is past the list
 }
 
-// Blocks that take part (each with at least one step), the first step of one,
-// and the block whose range holds step x.
-__device__ __forceinline__ int blocks_used(const DecodeArgs& a, int total) { return min(a.main_blocks, total); }
-__device__ __forceinline__ int block_first(int total, int b, int blocks) {
-  return int(int64_t(total) * b / blocks);
-}
-// the block whose range holds step x
-__device__ __forceinline__ int block_of(int total, int x, int blocks) {
-  return int((int64_t(x + 1) * blocks - 1) / total);
-}
+// How T steps are shared out: the first T % C blocks take one more than the
+// others.  Blocks past T take none.
+struct Split {
+  int q, r;   // T / C, T % C
+  __device__ __forceinline__ Split(int total, const FastDiv& blocks)
+      : q(int(fdiv(uint32_t(total), blocks))), r(total - int(fdiv(uint32_t(total), blocks)) * int(blocks.d)) {}
+  __device__ __forceinline__ int first(int b) const { return b * q + min(b, r); }
+  __device__ __forceinline__ int count(int b) const { return q + (b < r ? 1 : 0); }
+  __device__ __forceinline__ int block_of(int x) const {   // x < T
+    const int wide = r * (q + 1);
+    return x < wide ? x / (q + 1) : r + (x - wide) / q;
+  }
+};
 
-// A position in the list of steps: sequence, item of the sequence (key head
-// major, row block minor), step of the item.
+// A position in the list of steps: sequence, key head and row block of the
+// item, step of the item.
 struct Cursor {
   Span sp;
-  int s, it, c, nc;
+  const int32_t* table;   // the sequence's row of the page table
+  int s, g, blk, c, nc;
 };
 
 __device__ __forceinline__ void load_seq(const DecodeArgs& a, Cursor& u) {
   while (true) {   // sequences without a visible key have no steps
     u.sp = span_of(a, seq_len(a.c, a.seq_lens, u.s));
-    u.nc = u.sp.steps();
-    if (u.nc > 0 || u.s + 1 >= a.c.n_seqs) return;
+    u.nc = u.sp.steps(a.step_keys);
+    if (u.nc > 0 || u.s + 1 >= a.c.n_seqs) break;
     ++u.s;
   }
+  u.table = a.c.table + int64_t(u.s) * a.c.table_stride;
 }
 
 __device__ __forceinline__ void advance(const DecodeArgs& a, Cursor& u) {
   if (++u.c < u.nc) return;
   u.c = 0;
-  if (++u.it < a.c.H * a.n_blk) return;
-  u.it = 0;
+  if (++u.blk < a.n_blk) return;
+  u.blk = 0;
+  if (++u.g < a.c.H) return;
+  u.g = 0;
   if (u.s + 1 >= a.c.n_seqs) return;   // past the last step: not used
   ++u.s;
   load_seq(a, u);
@@ -182,347 +187,399 @@ __device__ __forceinline__ void advance(const DecodeArgs& a, Cursor& u) {
 // Entry x of a sequence's visible list -> its token.
 __device__ __forceinline__ int token_of(const Span& sp, int x) { return x < sp.se ? x : x - sp.se + sp.lo; }
 
-template <int MT, int kStages>
+// Shared memory of a block whose warps split into NR row tiles: 4 / NR key
+// tiles of 16 keys a step, each read by NR warps.
+template <int NR>
 struct DecSmem {
-  static constexpr int kQBytes = MT * 16 * int(kRowBytes);
-  // merge buffer: per warp 640 floats a 16-row tile (16 rows of 32 columns
-  // padded to 40, or 8 of 64 to 72, or 4 of 128 to 136)
-  static constexpr int kMergeFloats = MT * 640;
-  static constexpr int kOffQ = kStages * kStepBytes;
-  static constexpr int kOffMerge = kOffQ + kStages * kQBytes;
-  static constexpr int kOffMl = kOffMerge + kDecWarps * kMergeFloats * 4;
-  static constexpr int kOffMask = kOffMl + kDecWarps * MT * 16 * 8;
+  static constexpr int kKeyTiles = kDecWarps / NR;
+  static constexpr int kStepKeys = kKeyTiles * kTileKeys;
+  static constexpr int kStageBytes = kKeyTiles * 2 * kTileBytes;
+  static constexpr int kStages = kRingBytes / kStageBytes;
+  static constexpr int kOffMl = kRingBytes;
+  static constexpr int kOffMask = kOffMl + kDecWarps * 16 * 8;
   static constexpr int kBytes = kOffMask + kStages * kDecWarps * 4;
-  static_assert(kBytes <= 232448, "shared memory of one block");
+  // the stage an item's last step was in serves as the buffer its warps' O
+  // meet in: so many floats per warp
+  static constexpr int kMergeFloats = kStageBytes / 4 / kDecWarps;
+  static_assert(kDecPerSm * (kBytes + 1024) <= 228 * 1024, "blocks of one SM");
 };
 
-template <int MT, int kStages, bool kWeights>
-__global__ void __launch_bounds__(kDecThreads, 1) decode_paged_kernel(const __grid_constant__ DecodeArgs a) {
-  using SM = DecSmem<MT, kStages>;
+template <int NR, bool kWeights>
+__global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(const __grid_constant__ DecodeArgs a) {
+  using SM = DecSmem<NR>;
+  constexpr int kStages = SM::kStages, kKeyTiles = SM::kKeyTiles;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kt = warp % kKeyTiles, rt = warp / kKeyTiles;   // the warp's key tile and row tile
   const int per_step = a.c.H * a.n_blk;
+  // nothing is read before the launches ahead are complete, nor may the join
+  // read the lengths before
+  ptx::pdl_wait();
   ptx::pdl_launch_dependents();
 
-  const int total = total_steps<MainSteps>(a, per_step);
-  const int blocks = blocks_used(a, total);
-
-  if (int(blockIdx.x) < blocks) {
-    const int c0 = block_first(total, blockIdx.x, blocks);
-    const int n_steps = block_first(total, blockIdx.x + 1, blocks) - c0;   // >= 1
-    const Place pl = find_step<MainSteps>(a, per_step, c0);
+  const int total = total_steps(a, per_step);
+  const Split split(total, a.div_blocks);
+  const int n_steps = split.count(blockIdx.x);
+  const int c0 = split.first(blockIdx.x);
+  BlockRec& rec = a.recs[blockIdx.x];
+  if (n_steps == 0 && tid == 0) {
+    rec.n = 0;
+    rec.parts = 0;
+  }
+  if (n_steps > 0) {
     Cursor cu;   // the step computed next
-    cu.s = pl.s;
-    load_seq(a, cu);
-    cu.it = (c0 - pl.base) / cu.nc;
-    cu.c = (c0 - pl.base) - cu.it * cu.nc;
+    {
+      const Place pl = find_step(a, per_step, c0);
+      cu.s = pl.s;
+      load_seq(a, cu);
+      const int it = (c0 - pl.base) / cu.nc;
+      cu.c = (c0 - pl.base) - it * cu.nc;
+      cu.g = a.n_blk == 1 ? it : it / a.n_blk;
+      cu.blk = it - cu.g * a.n_blk;
+    }
+    if (tid == 0) {
+      rec.s = cu.s;
+      rec.g = cu.g;
+      rec.blk = cu.blk;
+      rec.c = cu.c;
+      rec.first = c0;
+      rec.n = n_steps;
+      rec.total = total;
+    }
     Cursor is = cu;   // the step copied next
     int issued = 0;
-    uint32_t q_slot_is = 0, q_slot = 0;   // Q ring position of the issued / computed item
-    float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge);
+    uint32_t st_is = 0, st = 0;   // stage of the issued / computed step
     float2* ml = reinterpret_cast<float2*>(smem + SM::kOffMl);
     uint32_t* vmask = reinterpret_cast<uint32_t*>(smem + SM::kOffMask);
 
-    // Copy this warp's 16 keys of step `is` into stage issued % kStages, and,
-    // where an item begins, its Q rows (all threads together).
+    // Rows of 256 bytes lie in shared memory as sixteen 16-byte pieces, piece
+    // p of row r at place p ^ (r % 8), so that eight rows' pieces of one
+    // column block fall into different banks.  Of the places a lane touches
+    // only four differ beyond a constant: x ^ 2c for c = 0..3.
+    constexpr int kCopies = 8 / NR;                          // row pairs of a tile this warp copies
+    constexpr int kDistinct = kCopies < 4 ? kCopies : 4;
+    uint32_t dofs[kDistinct], kofs[4], vofs[4];
+    {
+      const uint32_t hi = uint32_t(lane) >> 4, low = uint32_t(lane) & 7u, piece = uint32_t(lane) & 15u;
+      const uint32_t tile = sbase + uint32_t(kt) * (2 * kTileBytes);
+#pragma unroll
+      for (int c = 0; c < kDistinct; ++c) {
+        // copies: rows 2c + hi of the warp's share of the tile, piece `piece`
+        const uint32_t r = uint32_t(rt * (kTileKeys / NR) + 2 * c) + hi;
+        dofs[c] = tile + r * kRowBytes + ((piece ^ (r & 7u)) << 4);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // K operand: keys 0-7 and 8-15, column pieces 2kk and 2kk + 1
+        kofs[c] = tile + (low + (hi << 3)) * kRowBytes + ((((uint32_t(lane) >> 3) & 1u) ^ low ^ (2u * c)) << 4);
+        // V operand: keys 0-15, column pieces 2np and 2np + 1
+        vofs[c] = tile + kTileBytes + piece * kRowBytes + ((hi ^ low ^ (2u * c)) << 4);
+      }
+    }
+    const uint8_t* const k_lane = a.c.k + (lane & 15) * 16;
+    const uint8_t* const v_lane = a.c.v + (lane & 15) * 16;
+
+    // Copy this warp's share of its key tile of step `is` into its stage.
     auto issue = [&]() {
       if (issued < n_steps) {
-        const uint32_t st = uint32_t(issued) % kStages;
-        const int g = is.it / a.n_blk;
-        const int x0 = is.c * kStepKeys + warp * kTileKeys, x = x0 + (lane & 15);
-        bool ok = x < is.sp.span;
-        uint32_t unit = 0;
-        if (ok) {
-          const uint32_t j = uint32_t(token_of(is.sp, x));
-          const uint32_t page = page_of(a.c, is.s, j);
-          ok = page < a.c.n_pages;
-          if (ok) unit = row_unit(a.c, page, j, g);
-          else record(a.c, kBadPage);
-        }
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-        if (lane == 0) vmask[st * kDecWarps + warp] = mask;
-        const uint32_t dst = sbase + st * kStepBytes + uint32_t(warp) * (2 * kTileBytes);
-        const uint32_t piece = uint32_t(lane) & 15u;
+        const int x0 = is.c * SM::kStepKeys + kt * kTileKeys, x = x0 + (lane & 15);
         if (x0 < is.sp.span) {   // a tile past the list's end is not computed either
-#pragma unroll
-          for (int i = 0; i < kTileKeys / 2; ++i) {
-            const int kk = 2 * i + (lane >> 4);
-            const uint32_t un = __shfl_sync(0xffffffffu, unit, kk);
-            const uint32_t bytes = (mask >> kk) & 1u ? 16u : 0u;
-            const uint64_t off = uint64_t(un) * kRowBytes + piece * 16u;
-            const uint32_t d = dst + uint32_t(kk) * kRowBytes + ((piece ^ (uint32_t(kk) & 7u)) << 4);
-            ptx::cp_async16(d, a.c.k + off, bytes);
-            ptx::cp_async16(d + kTileBytes, a.c.v + off, bytes);
+          bool ok = x < is.sp.span;
+          uint32_t unit = 0;
+          if (ok) {
+            const uint32_t j = uint32_t(token_of(is.sp, x));
+            const uint32_t pg = fdiv(j, a.c.div_P);
+            const uint32_t page = uint32_t(is.table[pg]);
+            ok = page < a.c.n_pages;
+            unit = page * a.c.page_units + (j - pg * a.c.P) * uint32_t(a.c.H) + uint32_t(is.g);
+            if (!ok) record(a.c, kBadPage);
           }
+          const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
+          if (lane == 0) vmask[st_is * kDecWarps + warp] = mask;
+          const uint32_t so = st_is * SM::kStageBytes;
+          const int kk0 = rt * (kTileKeys / NR) + (lane >> 4);
+          unit = ok ? unit : 0u;
+          auto rows = [&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (i < kCopies) {
+              constexpr int kOff = (i / 4) * 8 * int(kRowBytes);   // rows 8 apart swizzle alike
+              const uint32_t d = dofs[i % kDistinct] + so;
+              const uint64_t off = uint64_t(__shfl_sync(0xffffffffu, unit, kk0 + 2 * i)) * kRowBytes;
+              if (mask == 0xFFFFu) {
+                ptx::cp_async16<kOff>(d, k_lane + off);
+                ptx::cp_async16<kOff + kTileBytes>(d, v_lane + off);
+              } else {   // rows that are not there are zeros
+                const uint32_t bytes = ((mask >> (kk0 + 2 * i)) & 1u) << 4;
+                ptx::cp_async16_fill<kOff>(d, k_lane + off, bytes);
+                ptx::cp_async16_fill<kOff + kTileBytes>(d, v_lane + off, bytes);
+              }
+            }
+          };
+          rows(std::integral_constant<int, 0>());
+          rows(std::integral_constant<int, 1>());
+          rows(std::integral_constant<int, 2>());
+          rows(std::integral_constant<int, 3>());
+          rows(std::integral_constant<int, 4>());
+          rows(std::integral_constant<int, 5>());
+          rows(std::integral_constant<int, 6>());
+          rows(std::integral_constant<int, 7>());
         }
-        if (issued == 0 || is.c == 0) {
-          if (issued > 0) q_slot_is = (q_slot_is + 1) % kStages;
-          const int blk = is.it - g * a.n_blk;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const int r = i * 16 + (tid >> 4);
-            const int row = blk * (MT * 16) + r;
-            const bool there = row < a.rows;
-            const int qi = there ? row / a.G : 0;
-            const int h = there ? g * a.G + row - qi * a.G : 0;
-            const uint32_t pc = uint32_t(tid) & 15u;
-            ptx::cp_async16(sbase + SM::kOffQ + q_slot_is * SM::kQBytes + uint32_t(r) * kRowBytes +
-                                ((pc ^ (uint32_t(r) & 7u)) << 4),
-                            a.q + (int64_t(is.s) * a.Lq + qi) * a.q_row + int64_t(h) * kRowBytes + pc * 16u,
-                            there ? 16u : 0u);
-          }
-        }
+        st_is = st_is + 1 == kStages ? 0 : st_is + 1;
         ++issued;
         if (issued < n_steps) advance(a, is);
       }
       ptx::cp_async_commit();
     };
 
-    // Q as A operands: in registers where one row tile leaves room, else read
-    // from shared memory in every step
-    constexpr bool kQRegs = MT == 1;
-    uint32_t qf[kQRegs ? MT : 1][8][4];
-    auto load_q = [&](uint32_t qb, int i, int kk, uint32_t (&r4)[4]) {
-      // matrices of an A tile: rows 0-7 / 8-15, then the next 8 columns
-      const uint32_t r = uint32_t(i * 16 + (lane & 15)), pc = uint32_t(2 * kk + (lane >> 4));
-      ptx::ldsm4(qb + r * kRowBytes + ((pc ^ (r & 7u)) << 4), r4);
-    };
-    float O[MT][16][4];
-    float m[MT][2], l[MT][2];
-    int row_hi[MT][2], row_lo[MT][2];   // this lane's rows (g, g + 8 of each tile): keys < hi, >= lo or a sink
+    uint32_t qf[8][4];   // the warp's 16 Q rows as A operands
+    float O[16][4];
+    float m[2], l[2];    // of rows lane / 4 and 8 + lane / 4
     int all_lo = 0, all_hi = 0;         // keys in [all_lo, all_hi) are visible to every row
     int frag_c0 = 0, frag_t0 = 0;       // step of the item, and of the block, this part of the item began at
     bool first = true;
 
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue();
 
+#pragma unroll 1
     for (int t = 0; t < n_steps; ++t) {
-      issue();
-      ptx::cp_async_wait<kStages - 1>();
-      __syncwarp();
-      const int g = cu.it / a.n_blk, blk = cu.it - g * a.n_blk;
-      const uint32_t qb = sbase + SM::kOffQ + q_slot * SM::kQBytes;
+      if constexpr (NR == 1) {
+        issue();
+        ptx::cp_async_wait<kStages - 1>();
+        __syncwarp();
+      } else {
+        // the warps of a key tile: all their shares of this step have landed,
+        // and all are done with the stage that is filled next
+        ptx::cp_async_wait<kStages - 2>();
+        ptx::named_sync(1 + kt, 32 * NR);
+        issue();
+      }
       if (first) {
-        __syncthreads();   // every warp's share of the item's Q rows has landed
         first = false;
         frag_c0 = cu.c;
         frag_t0 = t;
-        const int last_q = min(a.rows, (blk + 1) * (MT * 16)) - 1, first_q = blk * (MT * 16);
-        const int c_first = cu.sp.L - a.Lq + first_q / a.G, c_last = cu.sp.L - a.Lq + last_q / a.G;
-        all_hi = max(0, c_first + 1);
-        all_lo = a.window > 0 ? max(0, c_last - a.window + 1) : 0;
+        const int last_q = min(a.rows, (cu.blk + 1) * (NR * 16)) - 1, first_q = cu.blk * (NR * 16);
+        all_hi = max(0, cu.sp.L - a.Lq + int(fdiv(uint32_t(first_q), a.div_G)) + 1);
+        all_lo = a.window > 0 ? max(0, cu.sp.L - a.Lq + int(fdiv(uint32_t(last_q), a.div_G)) - a.window + 1) : 0;
+        // Q straight from global memory: its latency is a small part of an
+        // item's time, and the stages under way keep the memory busy
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          if constexpr (kQRegs) {
+        for (int e = 0; e < 2; ++e) {
+          const int row = cu.blk * (NR * 16) + rt * 16 + e * 8 + (lane >> 2);
+          const bool there = row < a.rows;
+          const int qi = there ? int(fdiv(uint32_t(row), a.div_G)) : 0;
+          const int h = there ? cu.g * a.G + row - qi * a.G : 0;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(
+              a.q + (int64_t(cu.s) * a.Lq + qi) * a.q_row + int64_t(h) * kRowBytes + (lane & 3) * 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) load_q(qb, i, kk, qf[i][kk]);
-          }
-#pragma unroll
-          for (int n = 0; n < 16; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) O[i][n][e] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            m[i][e] = -INFINITY;
-            l[i][e] = 0.f;
-            const int row = blk * (MT * 16) + i * 16 + e * 8 + (lane >> 2);
-            const int c = cu.sp.L - a.Lq + row / a.G;
-            row_hi[i][e] = row < a.rows ? max(0, c + 1) : 0;
-            row_lo[i][e] = a.window > 0 ? max(0, c - a.window + 1) : 0;
+          for (int kk = 0; kk < 8; ++kk) {
+            qf[kk][e] = there ? __ldg(src + 8 * kk) : 0u;
+            qf[kk][2 + e] = there ? __ldg(src + 8 * kk + 4) : 0u;
           }
         }
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) O[n][e] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
       }
 
-      const uint32_t st = uint32_t(t) % kStages;
-      const int x0 = cu.c * kStepKeys + warp * kTileKeys;
+      const int x0 = cu.c * SM::kStepKeys + kt * kTileKeys;
       if (x0 < cu.sp.span) {
         const uint32_t mask = vmask[st * kDecWarps + warp];
-        const uint32_t sk = sbase + st * kStepBytes + uint32_t(warp) * (2 * kTileBytes), sv = sk + kTileBytes;
-        // S = Q K^T: two chains of four products per 8-key tile and row tile
-        float S[MT][2][4], S2[MT][2][4];
+        const uint32_t so = st * SM::kStageBytes;
+        // S = Q K^T, 16 rows x 16 keys
+        float S[2][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][n][e] = S2[i][n][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          // matrices: keys 0-7 of columns 16kk.. and 16kk + 8.., then keys 8-15
-          uint32_t b[4];
-          const uint32_t r = uint32_t((lane & 7) + ((lane >> 4) << 3)), pc = uint32_t(2 * kk + ((lane >> 3) & 1));
-          ptx::ldsm4(sk + r * kRowBytes + ((pc ^ (r & 7u)) << 4), b);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t qa[4];
-            if constexpr (kQRegs) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) qa[e] = qf[i][kk][e];
-            } else {
-              load_q(qb, i, kk, qa);
-            }
-            ptx::mma_bf16(kk & 1 ? S2[i][0] : S[i][0], qa, b[0], b[1]);
-            ptx::mma_bf16(kk & 1 ? S2[i][1] : S[i][1], qa, b[2], b[3]);
-          }
-        }
+          for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+        auto s_step = [&](auto kc) {
+          constexpr int kk = decltype(kc)::value;
+          uint32_t b[4];   // keys 0-7 of columns 16kk.. and 16kk + 8.., then keys 8-15
+          ptx::ldsm4<(kk >> 2) * 128>(kofs[kk & 3] + so, b);
+          ptx::mma_bf16(S[0], qf[kk], b[0], b[1]);
+          ptx::mma_bf16(S[1], qf[kk], b[2], b[3]);
+        };
+        s_step(std::integral_constant<int, 0>());
+        s_step(std::integral_constant<int, 1>());
+        s_step(std::integral_constant<int, 2>());
+        s_step(std::integral_constant<int, 3>());
+        s_step(std::integral_constant<int, 4>());
+        s_step(std::integral_constant<int, 5>());
+        s_step(std::integral_constant<int, 6>());
+        s_step(std::integral_constant<int, 7>());
         // the tile holds tokens j0 .. j0 + 15 unless the list jumps from the
         // sinks to the window inside it; no mask is needed where every row sees all
         const int j0 = token_of(cu.sp, x0);
         const bool plain = mask == 0xFFFFu && (x0 >= cu.sp.se || x0 + kTileKeys <= cu.sp.se) &&
                            j0 + kTileKeys <= all_hi && (j0 >= all_lo || j0 + kTileKeys <= a.sinks);
-        uint32_t P[MT][4];
+        if (!plain) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][n][e] = (S[i][n][e] + S2[i][n][e]) * a.scale_log2;
-          if (!plain) {
+          for (int e = 0; e < 2; ++e) {
+            // the row sees keys <= c that are past c - window or among the sinks
+            const int row = cu.blk * (NR * 16) + rt * 16 + e * 8 + (lane >> 2);
+            const int c = row < a.rows ? cu.sp.L - a.Lq + int(fdiv(uint32_t(row), a.div_G)) : -1;
+            const int from = a.window > 0 ? c - a.window + 1 : 0;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kk = n * 8 + 2 * (lane & 3) + (e & 1);
+              for (int f = 0; f < 2; ++f) {
+                const int kk = n * 8 + 2 * (lane & 3) + f;
                 const int j = token_of(cu.sp, x0 + kk);
-                const bool vis = ((mask >> kk) & 1u) && j < row_hi[i][e >> 1] &&
-                                 (j >= row_lo[i][e >> 1] || j < a.sinks);
-                if (!vis) S[i][n][e] = -INFINITY;
+                const bool vis = ((mask >> kk) & 1u) && j <= c && (j >= from || j < a.sinks);
+                if (!vis) S[n][2 * e + f] = -INFINITY;
               }
           }
-          if constexpr (kWeights) {
-            const int64_t step = int64_t(c0) + t;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = i * 16 + e * 8 + (lane >> 2);
-              if (r < a.rows_blk) {
-                float* dst = a.scores + (step * a.rows_blk + r) * kStepKeys + warp * kTileKeys + 2 * (lane & 3);
-                *reinterpret_cast<float2*>(dst) = make_float2(S[i][0][2 * e], S[i][0][2 * e + 1]);
-                *reinterpret_cast<float2*>(dst + 8) = make_float2(S[i][1][2 * e], S[i][1][2 * e + 1]);
-              }
-            }
-          }
-          float mx[2];
+        }
+        if constexpr (kWeights) {
+          const int64_t step = int64_t(c0) + t;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(fmaxf(S[i][0][2 * e], S[i][0][2 * e + 1]), fmaxf(S[i][1][2 * e], S[i][1][2 * e + 1]));
+            const int r = rt * 16 + e * 8 + (lane >> 2);
+            if (r < a.rows_blk) {
+              float* dst = a.scores + (step * a.rows_blk + r) * SM::kStepKeys + kt * kTileKeys + 2 * (lane & 3);
+              *reinterpret_cast<float2*>(dst) = make_float2(S[0][2 * e] * a.scale_log2, S[0][2 * e + 1] * a.scale_log2);
+              *reinterpret_cast<float2*>(dst + 8) =
+                  make_float2(S[1][2 * e] * a.scale_log2, S[1][2 * e + 1] * a.scale_log2);
+            }
+          }
+        }
+        // a lane sees four of a row's sixteen scores; only where one of them
+        // outgrows the running maximum do the row's lanes find the tile's
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          mx[e] = a.scale_log2 * fmaxf(fmaxf(S[0][2 * e], S[0][2 * e + 1]), fmaxf(S[1][2 * e], S[1][2 * e + 1]));
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack)) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            const float nm = mx[e] > m[e] + kMaxSlack ? mx[e] : m[e];
+            f[e] = m[e] == nm ? 1.f : ptx::ex2_approx(m[e] - nm);
+            m[e] = nm;
+            l[e] *= f[e];
           }
-          const bool move = mx[0] > m[i][0] + kMaxSlack || mx[1] > m[i][1] + kMaxSlack;
-          if (__any_sync(0xffffffffu, move)) {
-            float f[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float nm = mx[e] > m[i][e] + kMaxSlack ? mx[e] : m[i][e];
-              f[e] = m[i][e] == nm ? 1.f : ptx::ex2_approx(m[i][e] - nm);
-              m[i][e] = nm;
-              l[i][e] *= f[e];
-            }
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              O[i][n][0] *= f[0];
-              O[i][n][1] *= f[0];
-              O[i][n][2] *= f[1];
-              O[i][n][3] *= f[1];
-            }
+          for (int n = 0; n < 16; ++n) {
+            O[n][0] *= f[0];
+            O[n][1] *= f[0];
+            O[n][2] *= f[1];
+            O[n][3] *= f[1];
           }
-          // P = exp2(S - m): summed in fp32, rounded to bf16 for P V (at most
-          // half a step of bf16, 2^-8 of each weight, as the output's own
-          // rounding).  S's accumulator layout is the A operand's as it stands.
-          const float u0 = m[i][0] == -INFINITY ? 0.f : m[i][0], u1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+        }
+        // P = exp2(S - m): summed in fp32, rounded to bf16 for P V (at most
+        // half a step of bf16, 2^-8 of each weight, as the output's own
+        // rounding).  S's accumulator layout is the A operand's as it stands.
+        uint32_t P[4];
+        const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float p0 = ptx::ex2_approx(S[i][n][0] - u0), p1 = ptx::ex2_approx(S[i][n][1] - u0);
-            const float p2 = ptx::ex2_approx(S[i][n][2] - u1), p3 = ptx::ex2_approx(S[i][n][3] - u1);
-            l[i][0] += p0 + p1;
-            l[i][1] += p2 + p3;
-            P[i][2 * n] = pack_bf16x2(p0, p1);
-            P[i][2 * n + 1] = pack_bf16x2(p2, p3);
-          }
+        for (int n = 0; n < 2; ++n) {
+          const float p0 = ptx::ex2_approx(fmaf(S[n][0], a.scale_log2, -u0));
+          const float p1 = ptx::ex2_approx(fmaf(S[n][1], a.scale_log2, -u0));
+          const float p2 = ptx::ex2_approx(fmaf(S[n][2], a.scale_log2, -u1));
+          const float p3 = ptx::ex2_approx(fmaf(S[n][3], a.scale_log2, -u1));
+          l[0] += p0 + p1;
+          l[1] += p2 + p3;
+          P[2 * n] = pack_bf16x2(p0, p1);
+          P[2 * n + 1] = pack_bf16x2(p2, p3);
         }
         // O += P V
-#pragma unroll
-        for (int np = 0; np < 8; ++np) {
-          // matrices: keys 0-7 / 8-15 of columns 16np.., then of 16np + 8..
-          uint32_t b[4];
-          const uint32_t r = uint32_t(lane & 15), pc = uint32_t(2 * np + (lane >> 4));
-          ptx::ldsm4_trans(sv + r * kRowBytes + ((pc ^ (r & 7u)) << 4), b);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            ptx::mma_bf16(O[i][2 * np], P[i], b[0], b[1]);
-            ptx::mma_bf16(O[i][2 * np + 1], P[i], b[2], b[3]);
-          }
-        }
+        auto o_step = [&](auto nc) {
+          constexpr int np = decltype(nc)::value;
+          uint32_t b[4];   // keys 0-7 / 8-15 of columns 16np.., then of 16np + 8..
+          ptx::ldsm4_trans<(np >> 2) * 128>(vofs[np & 3] + so, b);
+          ptx::mma_bf16(O[2 * np], P, b[0], b[1]);
+          ptx::mma_bf16(O[2 * np + 1], P, b[2], b[3]);
+        };
+        o_step(std::integral_constant<int, 0>());
+        o_step(std::integral_constant<int, 1>());
+        o_step(std::integral_constant<int, 2>());
+        o_step(std::integral_constant<int, 3>());
+        o_step(std::integral_constant<int, 4>());
+        o_step(std::integral_constant<int, 5>());
+        o_step(std::integral_constant<int, 6>());
+        o_step(std::integral_constant<int, 7>());
       }
-      __syncwarp();   // the warp is done with the stage issue() fills next
+      if constexpr (NR == 1) __syncwarp();   // the warp is done with the stage issue() fills next
 
       if (cu.c + 1 == cu.nc || t + 1 == n_steps) {
-        // ---- the item ends here, in this block: join the warps' parts ----
+        // ---- the item ends here, in this block: join the key tiles' parts ----
         const bool whole = frag_c0 == 0 && cu.c + 1 == cu.nc;
-        const int rows_here = min(a.rows - blk * (MT * 16), MT * 16);
+        const int rows_here = min(a.rows - cu.blk * (NR * 16), NR * 16);
+        const int part = frag_t0 == 0 ? 0 : 1;
+        const int64_t slot = (int64_t(blockIdx.x) * 2 + part) * a.rows_blk;
+        if (t + 1 == n_steps && tid == 0) {
+          // the item goes on in other blocks: this one joins it if it began here
+          rec.parts = frag_c0 == 0 && !whole ? split.block_of(c0 + t - cu.c + cu.nc - 1) - int(blockIdx.x) + 1 : 0;
+          rec.join_s = cu.s;
+          rec.join_g = cu.g;
+          rec.join_blk = cu.blk;
+          rec.slot = part;
+        }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 1);
-            l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], 2);
-            if ((lane & 3) == 0) ml[warp * (MT * 16) + i * 16 + e * 8 + (lane >> 2)] = make_float2(m[i][e], l[i][e]);
-          }
-        __syncthreads();
-        auto joined = [&](int r, float& M, float& sum) {
+        for (int e = 0; e < 2; ++e) {
+          l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+          l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+          if ((lane & 3) == 0) ml[warp * 16 + e * 8 + (lane >> 2)] = make_float2(m[e], l[e]);
+        }
+        __syncthreads();   // and every warp is done with the stage: it holds the O parts from here
+        auto joined = [&](int r, float& M, float& sum) {   // row r of the block, over its key tiles
+          const float2* x = ml + (r >> 4) * kKeyTiles * 16 + (r & 15);
           M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * (MT * 16) + r].x);
+          for (int w = 0; w < kKeyTiles; ++w) M = fmaxf(M, x[w * 16].x);
           sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < kDecWarps; ++w) {
-            const float2 x = ml[w * (MT * 16) + r];
-            sum += x.x == -INFINITY ? 0.f : x.y * ptx::ex2_approx(x.x - M);
-          }
+          for (int w = 0; w < kKeyTiles; ++w)
+            sum += x[w * 16].x == -INFINITY ? 0.f : x[w * 16].y * ptx::ex2_approx(x[w * 16].x - M);
         };
-        float f[MT][2];
+        float f[2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float M, sum;
-            joined(i * 16 + e * 8 + (lane >> 2), M, sum);
-            f[i][e] = m[i][e] == -INFINITY ? 0.f : ptx::ex2_approx(m[i][e] - M);
-          }
-        const int64_t slot = (int64_t(blockIdx.x) * 2 + (frag_t0 == 0 ? 0 : 1)) * a.rows_blk;
+        for (int e = 0; e < 2; ++e) {
+          float M, sum;
+          joined(rt * 16 + e * 8 + (lane >> 2), M, sum);
+          f[e] = m[e] == -INFINITY ? 0.f : ptx::ex2_approx(m[e] - M);
+        }
         if (tid < rows_here && (!whole || kWeights)) {
           float M, sum;
           joined(tid, M, sum);
           if (!whole)
             a.part_ml[slot + tid] = make_float2(M, sum);
           else
-            a.item_ml[(int64_t(cu.s) * per_step + cu.it) * a.rows_blk + tid] = make_float2(M, sum);
+            a.item_ml[(int64_t(cu.s) * per_step + cu.g * a.n_blk + cu.blk) * a.rows_blk + tid] = make_float2(M, sum);
         }
-        const int cw = rows_here <= 4 ? 128 : (rows_here <= 8 ? 64 : 32), pad = cw + 8;
+        // rows of cw columns at a time, padded by 8 floats so that four rows
+        // fall into different banks
+        float* const merge = reinterpret_cast<float*>(smem + st * SM::kStageBytes);
+        const int tile_rows = min(rows_here, 16);
+        int cw = 128;
+        while (tile_rows * (cw + 8) > SM::kMergeFloats) cw >>= 1;
+        const int pad = cw + 8;
         for (int cb = 0; cb < kHD; cb += cw) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int e = 0; e < 2; ++e) {
+            const int r = e * 8 + (lane >> 2);
+            if (rt * 16 + r < rows_here) {
+              float* dst = merge + warp * SM::kMergeFloats + r * pad + 2 * (lane & 3) - cb;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = i * 16 + e * 8 + (lane >> 2);
-              if (r < rows_here) {
-                float* dst = merge + warp * SM::kMergeFloats + r * pad + 2 * (lane & 3) - cb;
-#pragma unroll
-                for (int n = 0; n < 16; ++n)
-                  if (n * 8 >= cb && n * 8 < cb + cw)
-                    *reinterpret_cast<float2*>(dst + n * 8) =
-                        make_float2(O[i][n][2 * e] * f[i][e], O[i][n][2 * e + 1] * f[i][e]);
-              }
+              for (int n = 0; n < 16; ++n)
+                if (n * 8 >= cb && n * 8 < cb + cw)
+                  *reinterpret_cast<float2*>(dst + n * 8) = make_float2(O[n][2 * e] * f[e], O[n][2 * e + 1] * f[e]);
             }
+          }
           __syncthreads();
           for (int idx = tid; idx < rows_here * (cw / 2); idx += kDecThreads) {
             const int r = idx / (cw / 2), col = 2 * (idx - r * (cw / 2));
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-              const float2 x = *reinterpret_cast<const float2*>(merge + w * SM::kMergeFloats + r * pad + col);
+            for (int w = 0; w < kKeyTiles; ++w) {
+              const float2 x = *reinterpret_cast<const float2*>(
+                  merge + ((r >> 4) * kKeyTiles + w) * SM::kMergeFloats + (r & 15) * pad + col);
               sum.x += x.x;
               sum.y += x.y;
             }
@@ -530,7 +587,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_paged_kernel(const __gr
               float M, ls;
               joined(r, M, ls);
               const float inv = ls > 0.f ? 1.f / ls : 0.f;
-              const int row = blk * (MT * 16) + r, qi = row / a.G, h = g * a.G + row - qi * a.G;
+              const int row = cu.blk * (NR * 16) + r, qi = int(fdiv(uint32_t(row), a.div_G));
+              const int h = cu.g * a.G + row - qi * a.G;
               *reinterpret_cast<uint32_t*>(a.o + (int64_t(cu.s) * a.Lq + qi) * a.o_row + int64_t(h) * kRowBytes +
                                            (cb + col) * 2) = pack_bf16x2(sum.x * inv, sum.y * inv);
             } else {
@@ -540,8 +598,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_paged_kernel(const __gr
           __syncthreads();
         }
         first = true;
-        q_slot = (q_slot + 1) % kStages;
       }
+      st = st + 1 == kStages ? 0 : st + 1;
       if (t + 1 < n_steps) advance(a, cu);
     }
   }
@@ -560,142 +618,183 @@ __global__ void __launch_bounds__(kDecThreads, 1) decode_paged_kernel(const __gr
 // join: the items that lie in several blocks, and the weights
 // ---------------------------------------------------------------------------
 
-// The parts of the item with steps [x0, x1): blocks b0 .. b1 of the main
-// launch, the first one's part in slot `first`, the others' in slot 2 b.
-struct Parts {
-  int b0, b1;
-  int64_t first;
-};
-__device__ __forceinline__ Parts parts_of(int total, int blocks, int x0, int x1) {
-  Parts p;
-  p.b0 = block_of(total, x0, blocks);
-  p.b1 = block_of(total, x1 - 1, blocks);
-  p.first = int64_t(p.b0) * 2 + (block_first(total, p.b0, blocks) == x0 ? 0 : 1);
-  return p;
-}
-__device__ __forceinline__ int64_t part_row(const DecodeArgs& a, const Parts& p, int b, int r) {
-  return (b == p.b0 ? p.first : int64_t(b) * 2) * a.rows_blk + r;
-}
-
-// Running maximum and sum of row r of an item over its parts.
-__device__ __forceinline__ void join_ml(const DecodeArgs& a, const Parts& p, int r, float& M, float& sum) {
-  M = -INFINITY;
-  sum = 0.f;
-  for (int b = p.b0; b <= p.b1; ++b) M = fmaxf(M, a.part_ml[part_row(a, p, b, r)].x);
-  for (int b = p.b0; b <= p.b1; ++b) {
-    const float2 x = a.part_ml[part_row(a, p, b, r)];
-    sum += x.x == -INFINITY ? 0.f : x.y * ptx::ex2_approx(x.x - M);
-  }
+// Row r of part i of an item whose first part is slot `first` of the parts and
+// begins in block b0.
+__device__ __forceinline__ int64_t part_row(const DecodeArgs& a, int b0, int slot, int i, int r) {
+  return (int64_t(b0 + i) * 2 + (i == 0 ? slot : 0)) * a.rows_blk + r;
 }
 
 template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
-  extern __shared__ float2 row_ml[];   // weights: maximum and 1 / sum of the rows of the step's key head
-  const int tid = threadIdx.x;
-  const int per_step = a.c.H * a.n_blk;
-  const int total = total_steps<MainSteps>(a, per_step);
-  const int blocks = blocks_used(a, total);
-
-  Place pl = {0, 0};
-  int c0 = 0, c1 = 0;
-  if (int(blockIdx.x) < blocks) {
-    c0 = block_first(total, blockIdx.x, blocks);
-    c1 = block_first(total, blockIdx.x + 1, blocks);
-    pl = find_step<MainSteps>(a, per_step, c1 - 1);
-  }
+  __shared__ float4 part[kJoinThreads / 32][32];
+  __shared__ float2 part_sum[kJoinThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ptx::pdl_wait();   // the main launch's parts are written
-  if (int(blockIdx.x) < blocks) {
-    // the item this block's last step lies in, where it began here and goes on
-    const int nc = MainSteps::of(a, pl.s);
-    const int it = (c1 - 1 - pl.base) / nc, x0 = pl.base + it * nc, x1 = x0 + nc;
-    if (x1 > c1 && x0 >= c0) {
-      const Parts p = parts_of(total, blocks, x0, x1);
-      const int g = it / a.n_blk, blk = it - g * a.n_blk;
-      const int rows_here = min(a.rows - blk * a.rows_tile, a.rows_tile);
-      for (int idx = tid; idx < rows_here * (kHD / 4); idx += kJoinThreads) {
-        const int r = idx / (kHD / 4), col = 4 * (idx - r * (kHD / 4));
-        float M, ls;
-        join_ml(a, p, r, M, ls);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int b = p.b0; b <= p.b1; ++b) {
-          const int64_t at = part_row(a, p, b, r);
-          const float mb = a.part_ml[at].x;
-          const float f = mb == -INFINITY ? 0.f : ptx::ex2_approx(mb - M);
-          const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * kHD + col);
-          sum.x += x.x * f;
-          sum.y += x.y * f;
-          sum.z += x.z * f;
-          sum.w += x.w * f;
+  ptx::pdl_launch_dependents();
+  const BlockRec rec = a.recs[blockIdx.x];
+
+  if (rec.parts > 0) {
+    // Main block b = blockIdx.x holds the item's first part.  A row is joined
+    // by `per` warps (all eight where there is one row), each with every
+    // per-th part; they meet in order in shared memory.
+    const int per = a.rows_blk == 1 ? 8 : (a.rows_blk == 2 ? 4 : (a.rows_blk <= 4 ? 2 : 1));
+    const int b0 = blockIdx.x, n = rec.parts;
+    const int rows_here = min(a.rows - rec.join_blk * a.rows_tile, a.rows_tile);
+    const int r = int(blockIdx.y) * (8 / per) + warp / per, w0 = warp % per;
+    float M = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows_here) {
+      for (int i0 = w0; i0 < n; i0 += 32 * per) {   // 32 parts at a time, one a lane
+        const int mine = i0 + lane * per;
+        float2 x = make_float2(-INFINITY, 0.f);
+        if (mine < n) x = a.part_ml[part_row(a, b0, rec.slot, mine, r)];
+        float nm = x.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+        nm = fmaxf(nm, M);
+        const float old = M == nm ? 1.f : ptx::ex2_approx(M - nm);   // 0 for the first
+        const float f = x.x == -INFINITY ? 0.f : ptx::ex2_approx(x.x - nm);
+        M = nm;
+        float add = f * x.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+        sum = sum * old + add;
+        acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+        const int count = min(32, (n - i0 + per - 1) / per);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+          const float g = __shfl_sync(0xffffffffu, f, i);
+          const float4 y = *reinterpret_cast<const float4*>(
+              a.part_o + part_row(a, b0, rec.slot, i0 + i * per, r) * kHD + 4 * lane);
+          acc.x += y.x * g;
+          acc.y += y.y * g;
+          acc.z += y.z * g;
+          acc.w += y.w * g;
         }
-        const float inv = ls > 0.f ? 1.f / ls : 0.f;
-        const int row = blk * a.rows_tile + r, qi = row / a.G, h = g * a.G + row - qi * a.G;
-        *reinterpret_cast<uint2*>(a.o + (int64_t(pl.s) * a.Lq + qi) * a.o_row + int64_t(h) * kRowBytes + col * 2) =
-            make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
       }
+    }
+    if (per > 1) {
+      part[warp][lane] = acc;
+      if (lane == 0) part_sum[warp] = make_float2(M, sum);
+      __syncthreads();
+      if (w0 == 0) {
+        float top = M;
+        for (int w = 1; w < per; ++w) top = fmaxf(top, part_sum[warp + w].x);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum = 0.f;
+        for (int w = 0; w < per; ++w) {
+          const float2 s = part_sum[warp + w];
+          const float f = s.x == -INFINITY ? 0.f : ptx::ex2_approx(s.x - top);
+          const float4 y = part[warp + w][lane];
+          sum += s.y * f;
+          acc.x += y.x * f;
+          acc.y += y.y * f;
+          acc.z += y.z * f;
+          acc.w += y.w * f;
+        }
+      }
+    }
+    if (r < rows_here && w0 == 0) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int row = rec.join_blk * a.rows_tile + r, qi = int(fdiv(uint32_t(row), a.div_G));
+      const int h = rec.join_g * a.G + row - qi * a.G;
+      *reinterpret_cast<uint2*>(a.o + (int64_t(rec.join_s) * a.Lq + qi) * a.o_row + int64_t(h) * kRowBytes + lane * 8) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     }
   }
 
   if constexpr (kWeights) {
-    // p = exp2(score - maximum) / sum, added up over a token's rows in their
-    // order; one thread a token, the scores of 128 tokens of a row side by side
-    const int all = total_steps<TokenSteps>(a, a.c.H);
-    const int w0 = block_first(all, blockIdx.x, gridDim.x), w1 = block_first(all, blockIdx.x + 1, gridDim.x);
-    if (w0 == w1) return;
-    Place wp = find_step<TokenSteps>(a, a.c.H, w0);
-    int s = wp.s, at = w0 - wp.base;   // step of the sequence
-    int main_base = 0;                 // main steps before sequence s
-    for (int i = tid & 31; i < s; i += 32) main_base += MainSteps::of(a, i) * per_step;
-    main_base = __reduce_add_sync(0xffffffffu, main_base);
-    int loaded = -1;
-    for (int w = w0; w < w1; ++w, ++at) {
-      int ns = TokenSteps::of(a, s);
-      while (at >= ns * a.c.H) {
-        at -= ns * a.c.H;
-        main_base += MainSteps::of(a, s) * per_step;
-        ns = TokenSteps::of(a, ++s);
-        loaded = -1;
+    // The steps of main block b once more, a step to a warp, of each item's
+    // first row block only: p = exp2(score - maximum) / sum, added up over the
+    // token's rows in their order, lane i taking tokens 2i and 2i + 1 (64 keys
+    // a step; with fewer only the first lanes work).  Tokens that no query
+    // sees are copied, shared out over the item's steps.
+    if (rec.n == 0) return;
+    const Split split(rec.total, a.div_blocks);
+    Cursor cu;
+    cu.s = rec.s;
+    cu.g = rec.g;
+    cu.blk = rec.blk;
+    cu.c = rec.c;
+    load_seq(a, cu);
+    const int stride = int(gridDim.y) * (kJoinThreads / 32);
+    int loaded_x0 = -1, loaded_blk = -1;
+    float2 mr = make_float2(0.f, 0.f);   // lane r: maximum and 1 / sum of row r of the row block
+    int skip = int(blockIdx.y) * (kJoinThreads / 32) + warp;
+    for (int t = skip; t < rec.n; t += stride) {
+      // forward to step t
+      cu.c += skip;
+      skip = stride;
+      while (cu.c >= cu.nc) {
+        cu.c -= cu.nc;
+        if (++cu.blk < a.n_blk) continue;
+        cu.blk = 0;
+        if (++cu.g < a.c.H) continue;
+        cu.g = 0;
+        ++cu.s;
+        load_seq(a, cu);
       }
-      const Span sp = span_of(a, seq_len(a.c, a.seq_lens, s));
-      const int nc = sp.steps();
-      const int h = at / ns;
-      if (h != loaded) {
-        __syncthreads();   // the last head's rows are no longer read
-        for (int r = tid; r < a.rows; r += kJoinThreads) {
-          const int blk = r / a.rows_tile, rb = r - blk * a.rows_tile;
-          const int x0 = main_base + (h * a.n_blk + blk) * nc;
-          const Parts p = parts_of(total, blocks, x0, x0 + nc);
-          float M, ls;
-          if (p.b0 == p.b1) {
-            const float2 x = a.item_ml[(int64_t(s) * per_step + h * a.n_blk + blk) * a.rows_blk + rb];
-            M = x.x;
-            ls = x.y;
-          } else {
-            join_ml(a, p, rb, M, ls);
-          }
-          row_ml[r] = ls > 0.f ? make_float2(M, 1.f / ls) : make_float2(0.f, 0.f);
-        }
-        __syncthreads();
-        loaded = h;
-      }
-      const int j = (at - h * ns) * kWeightTokens + tid;
-      if (j >= sp.L) continue;
-      const int64_t out = (int64_t(s) * a.c.H + h) * a.c.capacity + j;
-      const float before = a.weight_in ? a.weight_in[out] : 0.f;
-      float sum = 0.f;
-      if (j < sp.se || j >= sp.lo) {
-        const int x = j < sp.se ? j : j - sp.lo + sp.se;
-        for (int blk = 0; blk < a.n_blk; ++blk) {
-          const int64_t step = int64_t(main_base) + (h * a.n_blk + blk) * nc + x / kStepKeys;
-          const float* sc = a.scores + step * a.rows_blk * kStepKeys + x % kStepKeys;
-          const int rows_here = min(a.rows - blk * a.rows_tile, a.rows_tile);
+      if (cu.blk != 0) continue;
+      const int64_t out = (int64_t(cu.s) * a.c.H + cu.g) * a.c.capacity;
+      const int x = cu.c * a.step_keys + 2 * lane;
+      const bool live = 2 * lane < a.step_keys;
+      float2 sum = make_float2(0.f, 0.f);
+      for (int blk = 0; blk < a.n_blk; ++blk) {
+        const int x0 = rec.first + t - cu.c + blk * cu.nc;   // the item's first step in the whole list
+        const int rows_here = min(a.rows - blk * a.rows_tile, a.rows_tile);
+        for (int r0 = 0; r0 < rows_here; r0 += 32) {
+          if (x0 != loaded_x0 || r0 != loaded_blk) {
+            loaded_x0 = x0;
+            loaded_blk = r0;
+            const int r = r0 + lane;
+            mr = make_float2(0.f, 0.f);
+            if (r < rows_here) {
+              const int b0 = split.block_of(x0), n = split.block_of(x0 + cu.nc - 1) - b0 + 1;
+              const int slot = split.first(b0) == x0 ? 0 : 1;
+              float M = -INFINITY, ls = 0.f;
+              if (n == 1) {
+                const float2 y = a.item_ml[(int64_t(cu.s) * a.c.H + cu.g) * a.n_blk * a.rows_blk +
+                                           int64_t(blk) * a.rows_blk + r];
+                M = y.x;
+                ls = y.y;
+              } else {
 #pragma unroll 4
-          for (int r = 0; r < rows_here; ++r) {
-            const float2 mr = row_ml[blk * a.rows_tile + r];
-            sum += ptx::ex2_approx(sc[int64_t(r) * kStepKeys] - mr.x) * mr.y;
+                for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_ml[part_row(a, b0, slot, i, r)].x);
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) {
+                  const float2 y = a.part_ml[part_row(a, b0, slot, i, r)];
+                  ls += y.x == -INFINITY ? 0.f : y.y * ptx::ex2_approx(y.x - M);
+                }
+              }
+              if (ls > 0.f) mr = make_float2(M, 1.f / ls);
+            }
+          }
+          const float* sc = a.scores + ((int64_t(x0) + cu.c) * a.rows_blk + r0) * a.step_keys + 2 * lane;
+          const int rows = min(rows_here - r0, 32);
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r) {
+            const float M = __shfl_sync(0xffffffffu, mr.x, r), inv = __shfl_sync(0xffffffffu, mr.y, r);
+            if (live) {
+              const float2 y = *reinterpret_cast<const float2*>(sc + int64_t(r) * a.step_keys);
+              sum.x += ptx::ex2_approx(y.x - M) * inv;
+              sum.y += ptx::ex2_approx(y.y - M) * inv;
+            }
           }
         }
       }
-      a.weight_out[out] = before + sum;
+      auto store = [&](int xx, float add) {
+        if (live && xx < cu.sp.span) {
+          const int64_t at = out + token_of(cu.sp, xx);
+          a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + add;
+        }
+      };
+      store(x, sum.x);
+      store(x + 1, sum.y);
+      if (cu.sp.lo > cu.sp.se && a.weight_in != a.weight_out) {
+        const int64_t gap = cu.sp.lo - cu.sp.se;
+        const int64_t from = cu.sp.se + gap * cu.c / cu.nc, to = cu.sp.se + gap * (cu.c + 1) / cu.nc;
+        for (int64_t j = from + lane; j < to; j += 32) a.weight_out[out + j] = a.weight_in ? a.weight_in[out + j] : 0.f;
+      }
     }
   }
 }
@@ -705,7 +804,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
 // ---------------------------------------------------------------------------
 struct DecodeShape {
   int64_t rows, rows_tile, rows_blk, n_blk, items, steps, blocks;
-  size_t part_o, part_ml, item_ml, scores, bytes;   // offsets into the workspace, and its size
+  int64_t step_keys;
+  size_t part_o, part_ml, recs, item_ml, scores, bytes;   // offsets into the workspace, and its size
 };
 
 static rkv_status decode_shape(const rkv_paged_cache* c, int32_t Hq, int32_t Lq, bool weights, DecodeShape& d) {
@@ -714,46 +814,60 @@ static rkv_status decode_shape(const rkv_paged_cache* c, int32_t Hq, int32_t Lq,
     return fail(RKV_ERR_INVALID_ARG, "Lq %d must be in [1, %d]", Lq, RKV_DECODE_MAX_LQ);
   d.rows = int64_t(Lq) * (Hq / c->H);
   if (d.rows > kMaxRows) return fail(RKV_ERR_UNSUPPORTED, "more than %d query rows to a key head", kMaxRows);
-  d.rows_tile = d.rows <= 16 ? 16 : 32;
+  // a row block is as many 16-row tiles as the rows need, up to the four that
+  // a block's warps can take
+  d.rows_tile = d.rows <= 16 ? 16 : (d.rows <= 32 ? 32 : 64);
+  d.step_keys = 1024 / d.rows_tile;
   d.rows_blk = std::min(d.rows, d.rows_tile);
   d.n_blk = (d.rows + d.rows_tile - 1) / d.rows_tile;
   d.items = int64_t(c->n_seqs) * c->H * d.n_blk;
-  d.steps = d.items * ((capacity(c) + kStepKeys - 1) / kStepKeys);
+  d.steps = d.items * ((capacity(c) + d.step_keys - 1) / d.step_keys);
   // step counts are 32-bit, and so is Lq * Hq * 16 in the zero fill
   if (d.steps >= (int64_t(1) << 30) || int64_t(c->n_seqs) * Lq >= (int64_t(1) << 31) || int64_t(Hq) * Lq >= (1 << 26))
     return fail(RKV_ERR_UNSUPPORTED, "too many sequences, heads and tokens for one launch");
-  d.blocks = std::min<int64_t>(sm_count(), std::max<int64_t>(d.steps, 1));
+  d.blocks = std::min<int64_t>(kDecPerSm * sm_count(), std::max<int64_t>(d.steps, 1));
   auto up = [](size_t x) { return (x + 15) / 16 * 16; };
   d.part_o = 0;
   d.part_ml = d.part_o + up(size_t(d.blocks * 2 * d.rows_blk) * kHD * 4);
-  d.item_ml = d.part_ml + up(size_t(d.blocks * 2 * d.rows_blk) * 8);
+  d.recs = d.part_ml + up(size_t(d.blocks * 2 * d.rows_blk) * 8);
+  d.item_ml = d.recs + size_t(d.blocks) * sizeof(BlockRec);
   d.scores = d.item_ml + (weights ? up(size_t(d.items * d.rows_blk) * 8) : 0);
-  d.bytes = d.scores + (weights ? size_t(d.steps * d.rows_blk) * kStepKeys * 4 : 0);
+  d.bytes = d.scores + (weights ? size_t(d.steps * d.rows_blk * d.step_keys) * 4 : 0);
   return RKV_OK;
 }
 
-template <int MT, int kStages, bool kWeights>
-static rkv_status launch_decode(const DecodeArgs& a, cudaStream_t cs) {
-  auto kern = decode_paged_kernel<MT, kStages, kWeights>;
-  constexpr int smem = DecSmem<MT, kStages>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_paged_kernel)");
-  kern<<<uint32_t(a.main_blocks), kDecThreads, smem, cs>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "decode_paged_kernel launch");
+// Launch with the stream's previous launch allowed to overlap its end (the
+// kernels wait for it before they read anything).
+template <class Kernel>
+static cudaError_t launch_overlapped(Kernel kern, dim3 grid, int threads, size_t smem, cudaStream_t cs,
+                                     const DecodeArgs& a) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  // the weights pass takes more blocks than the join needs
-  cfg.gridDim = dim3(uint32_t(kWeights ? 4 * sm_count() : a.main_blocks));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = kWeights ? size_t(a.rows) * 8 : 0;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(uint32_t(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = cs;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_join_kernel<kWeights>, a);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int NR, bool kWeights>
+static rkv_status launch_decode(const DecodeArgs& a, cudaStream_t cs) {
+  auto kern = decode_paged_kernel<NR, kWeights>;
+  constexpr int smem = DecSmem<NR>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_paged_kernel)");
+  e = launch_overlapped(kern, dim3(uint32_t(a.main_blocks)), kDecThreads, smem, cs, a);
+  if (e != cudaSuccess) return cuda_fail(e, "decode_paged_kernel launch");
+  // a block per main block and eight rows of a row block (its warps: see the
+  // kernel); the weights pass shares a main block's steps out over them
+  const int rows = a.rows_blk <= 4 ? 1 : (a.rows_blk + 7) / 8;
+  const dim3 grid(uint32_t(a.main_blocks), uint32_t(kWeights ? std::max(rows, 2) : rows));
+  e = launch_overlapped(decode_join_kernel<kWeights>, grid, kJoinThreads, 0, cs, a);
   if (e != cudaSuccess) return cuda_fail(e, "decode_join_kernel launch");
   return RKV_OK;
 }
@@ -824,20 +938,30 @@ extern "C" rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + d.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + d.part_ml);
+  a.recs = reinterpret_cast<BlockRec*>(ws + d.recs);
   a.item_ml = reinterpret_cast<float2*>(ws + d.item_ml);
   a.scores = reinterpret_cast<float*>(ws + d.scores);
   a.scale_log2 = float(double(softmax_scale) * 1.4426950408889634);
   a.Hq = Hq;
   a.Lq = Lq;
   a.G = Hq / cache->H;
+  a.div_G = make_fastdiv(uint32_t(a.G));
   a.rows = int32_t(d.rows);
   a.rows_tile = int32_t(d.rows_tile);
+  a.step_keys = int32_t(d.step_keys);
   a.rows_blk = int32_t(d.rows_blk);
   a.n_blk = int32_t(d.n_blk);
   a.window = window;
   a.sinks = sinks;
   a.main_blocks = int32_t(d.blocks);
+  a.div_blocks = make_fastdiv(uint32_t(d.blocks));
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (d.rows_tile == 16) return weight_out ? launch_decode<1, 3, true>(a, cs) : launch_decode<1, 3, false>(a, cs);
-  return weight_out ? launch_decode<2, 2, true>(a, cs) : launch_decode<2, 2, false>(a, cs);
+  if (weight_out) {
+    return d.rows_tile == 16   ? launch_decode<1, true>(a, cs)
+           : d.rows_tile == 32 ? launch_decode<2, true>(a, cs)
+                               : launch_decode<4, true>(a, cs);
+  }
+  return d.rows_tile == 16   ? launch_decode<1, false>(a, cs)
+         : d.rows_tile == 32 ? launch_decode<2, false>(a, cs)
+                             : launch_decode<4, false>(a, cs);
 }

@@ -99,6 +99,11 @@ __device__ __forceinline__ bool named_sync_and(uint32_t id, uint32_t count, bool
   return r != 0;
 }
 
+// Named barrier over `count` threads (a multiple of 32) of this CTA.
+__device__ __forceinline__ void named_sync(uint32_t id, uint32_t count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // ---- shared memory by 32-bit address -------------------------------------------
 // (volatile: issued in program order, so a batch's loads stay grouped and
 // register pressure stays bounded)
@@ -162,11 +167,19 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---- asynchronous 16-byte copies (per thread) ----------------------------------
-// Global -> shared memory, `bytes` (16 or 0) of the 16 read and the rest
-// zero-filled; both addresses 16-byte aligned.  With 0 the source is not read.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+// Global -> shared memory at dst + kOff, both addresses 16-byte aligned.
+template <int kOff>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0 + %2], [%1], 16;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "n"(kOff)
+               : "memory");
+}
+// The same of `bytes` (16 or 0) bytes, the rest zero-filled; with 0 the source
+// is not read.
+template <int kOff>
+__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0 + %2], [%1], 16, %3;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "n"(kOff), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -177,17 +190,20 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // ---- warp-level matrix instructions (few-row products) --------------------------
-// Four 8x8 16-bit matrices; lane i gives the address of row i % 8 of matrix i / 8.
+// Four 8x8 16-bit matrices; lane i gives the address of row i % 8 of matrix
+// i / 8, to which kOff bytes are added.
+template <int kOff>
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(kOff)
                : "memory");
 }
+template <int kOff>
 __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
+               : "r"(addr), "n"(kOff)
                : "memory");
 }
 // c (16 x 8, fp32) += a (16 x 16, bf16, row-major) * b (16 x 8, bf16, column-major)
