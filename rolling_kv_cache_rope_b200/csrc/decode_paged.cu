@@ -836,32 +836,12 @@ static rkv_status decode_shape(const rkv_paged_cache* c, int32_t Hq, int32_t Lq,
   return RKV_OK;
 }
 
-// Launch with the stream's previous launch allowed to overlap its end (the
-// kernels wait for it before they read anything).
-template <class Kernel>
-static cudaError_t launch_overlapped(Kernel kern, dim3 grid, int threads, size_t smem, cudaStream_t cs,
-                                     const DecodeArgs& a) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(uint32_t(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = cs;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
-  return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
 template <int NR, bool kWeights>
 static rkv_status launch_decode(const DecodeArgs& a, cudaStream_t cs) {
-  auto kern = decode_paged_kernel<NR, kWeights>;
   constexpr int smem = DecSmem<NR>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<decode_paged_kernel<NR, kWeights>>(smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(decode_paged_kernel)");
-  e = launch_overlapped(kern, dim3(uint32_t(a.main_blocks)), kDecThreads, smem, cs, a);
+  e = launch_overlapped(decode_paged_kernel<NR, kWeights>, dim3(uint32_t(a.main_blocks)), kDecThreads, smem, cs, a);
   if (e != cudaSuccess) return cuda_fail(e, "decode_paged_kernel launch");
   // a block per main block and eight rows of a row block (its warps: see the
   // kernel); the weights pass shares a main block's steps out over them

@@ -17,9 +17,13 @@ namespace paged {
 // host checks
 // ---------------------------------------------------------------------------
 int sm_count() {
+  static std::atomic<int> known[64];   // by device
   int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return n;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 148;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 static int64_t page_bytes(const rkv_paged_cache* c) { return int64_t(c->page_tokens) * c->H * kRowBytes; }
@@ -105,6 +109,8 @@ constexpr int kInsertUnroll = 4;
 
 __global__ void __launch_bounds__(kInsertThreads) paged_insert_kernel(const __grid_constant__ InsertArgs a) {
   const uint32_t first = blockIdx.x * uint32_t(kInsertThreads * kInsertUnroll) + threadIdx.x;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   uint4 kv[kInsertUnroll], vv[kInsertUnroll];
   uint64_t dst[kInsertUnroll];   // byte offset in the pools, or ~0: nothing to write
 #pragma unroll
@@ -142,6 +148,21 @@ __global__ void __launch_bounds__(kInsertThreads) paged_insert_kernel(const __gr
 
 // ---------------------------------------------------------------------------
 // evict
+//
+// Bound: reading weight and pos (8 bytes a token and key head) and, out of
+// place, writing them; then the rows that move (1 KB each).  Two ways to find
+// the tokens to drop, by how many there are (E = L - budget):
+//   E <= kFew   E rounds of a block-wide minimum over (key, index), about 0.1 us
+//               a round, and the block moves the rows itself: a decode step's
+//               eviction is one launch
+//   otherwise   radix selection of the budget-th largest key, 11 bits a pass,
+//               then lists of the places that fall free and of the tokens that
+//               move into them; a second launch moves the rows over all SMs
+//               (by the selecting blocks themselves 24 heads of 32,760 tokens
+//               cut to 7,800 took 66 us against 59)
+// A head's tokens are shared out over a cluster of blocks where there are too
+// few heads and sequences to fill the machine; the blocks' histograms and
+// counts meet in distributed shared memory.
 // ---------------------------------------------------------------------------
 struct EvictArgs {
   CacheDev c;
@@ -154,17 +175,22 @@ struct EvictArgs {
   int32_t* pos_out;
   int32_t budget, sinks, recent;
   int32_t in_place;
-  int32_t smem_keys;   // keys of one head that fit shared memory; the rest are formed again in each pass
+  int32_t lens_here;   // the selection writes seq_lens_out (no other block still reads seq_lens there)
+  int32_t cluster;     // blocks a head's tokens are shared out over
+  int32_t smem_keys;   // keys of one block that fit shared memory; the rest are formed again in each pass
   int32_t max_moves;   // moves one head can need: min(budget, capacity - budget)
-  int32_t* count;      // [n_seqs * H] moves of each head
-  int32_t* src;        // [n_seqs * H][max_moves] token each move takes
+  int32_t vec;         // heads' scores start on 16-byte boundaries
+  int32_t* count;      // [n_seqs * H] moves of each head left to the second launch
+  int32_t* src;        // [n_seqs * H][max_moves] token, then row each move takes
   int32_t* dst;        // ... and where it goes
   int32_t blocks_per_item;
 };
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kHistCopies = 4;
+constexpr int kBins = 2048;
+constexpr int kFew = 16;
+constexpr int kMaxCluster = 8;
 
 // Order of the keep rule as an unsigned number: protected tokens above every
 // weight, larger weights above smaller, -0 = 0, NaN below every number.
@@ -175,152 +201,343 @@ __device__ __forceinline__ uint32_t keep_key(float w, int pos, int sinks, int64_
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the block of one value a thread; `total` receives
-// the sum.  `warp_sums` holds kSelWarps words.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t inc = v;
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {   // inclusive
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += o;
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (int(threadIdx.x & 31) >= d) v += o;
   }
-  __syncthreads();   // warp_sums of an earlier scan are read
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  uint32_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const uint32_t x = warp_sums[w];
-    before += w < warp ? x : 0u;
-    total += x;
-  }
-  return before + inc - v;
+  return v;
 }
 
-// One head of one sequence per block: the key of the budget-th largest token
-// by radix selection, 8 bits a pass, then the lists of places that fall free
-// and of tokens that move into them.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __grid_constant__ EvictArgs a) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[kHistCopies][256];
+  __shared__ uint32_t hist[kBins];     // this block's keys by bin
+  __shared__ uint32_t bins[3][kBins];  // the cluster's, one for each pass
   __shared__ uint32_t warp_sums[kSelWarps];
-  __shared__ uint32_t found[2];
-  const int item = blockIdx.x, tid = threadIdx.x;
-  const int s = item / a.c.H;
-  ptx::pdl_launch_dependents();   // the move kernel's blocks may take their places; they wait for this grid's end
+  __shared__ uint32_t found[3];
+  __shared__ uint32_t block_sums[3][kMaxCluster];   // free places, moves and ties of each block
+  __shared__ uint64_t lowest[2][kSelWarps];
+  __shared__ int32_t few_src[kFew], few_dst[kFew], dropped[kFew];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cs = a.cluster, rank = cs > 1 ? int(ptx::cluster_ctarank()) : 0;
+  const int item = int(blockIdx.x) / cs;
+  const int s = item / a.c.H, h = item - s * a.c.H;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   const int L = seq_len(a.c, a.seq_lens, s);
   const int64_t base = int64_t(item) * a.c.capacity;
   const float* weight = a.weight + base;
   const int32_t* pos = a.pos + base;
   float* weight_out = a.weight_out + base;
   int32_t* pos_out = a.pos_out + base;
-  if (L <= a.budget) {
-    if (!a.in_place)
-      for (int j = tid; j < L; j += kSelThreads) {
-        weight_out[j] = weight[j];
-        pos_out[j] = pos[j];
-      }
-    if (tid == 0) a.count[item] = 0;
-    return;
+  const int E = L - a.budget;
+  const bool few = cs == 1 && E <= kFew;
+  if (tid == 0 && rank == 0) {
+    if (E <= 0 || few) a.count[item] = 0;
+    if (a.lens_here && h == 0) a.seq_lens_out[s] = min(L, a.budget);
   }
-  const int64_t recent_from = int64_t(a.next_pos[s]) - a.recent;
-  auto form_key = [&](int j) { return keep_key(weight[j], pos[j], a.sinks, recent_from); };
-  auto key = [&](int j) { return j < a.smem_keys ? keys[j] : form_key(j); };
-  for (int j = tid; j < min(L, a.smem_keys); j += kSelThreads) keys[j] = form_key(j);
+  if (E <= 0 && a.in_place) return;
 
-  uint32_t prefix = 0, mask = 0, want = uint32_t(a.budget);   // rank, from the top, among keys that share `prefix`
-  uint32_t equal = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kHistCopies * 256; i += kSelThreads) hist[i >> 8][i & 255] = 0;
-    __syncthreads();
-    for (int j = tid; j < L; j += kSelThreads) {
-      const uint32_t k = key(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(tid >> 5) & (kHistCopies - 1)][(k >> shift) & 255u], 1u);
+  auto sync = [&]() {
+    if (cs > 1) {
+      ptx::cluster_arrive();
+      ptx::cluster_wait();
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
-    if (tid < 32) {
-      // lane i sums bins 255 - 8i .. 248 - 8i, from the top
-      uint32_t n[8], sum = 0;
+  };
+  if (cs > 1 && E > 0) {
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) bins[0][i] = 0;
+    ptx::cluster_arrive();   // waited for before the first block adds to another's
+  }
+  // this block's tokens: [j0, j1)
+  const int seg = ((L + cs - 1) / cs + 31) & ~31;
+  const int j0 = min(L, rank * seg), j1 = min(L, j0 + seg);
+  const int64_t recent_from = int64_t(a.next_pos[s]) - a.recent;
+  auto key = [&](int j) {
+    return j - j0 < a.smem_keys ? keys[j - j0] : keep_key(weight[j], pos[j], a.sinks, recent_from);
+  };
+  // the lowest key of the thread's tokens; of equal ones the highest index
+  uint64_t low = ~uint64_t(0);
+  auto packed = [](uint32_t k, int j) { return uint64_t(k) << 32 | uint32_t(~j); };
+  // a thread takes four tokens in a row at a time, two times four in flight
+  constexpr int kBatch = 2;
+  for (int q = tid; j0 + 4 * q < j1; q += kBatch * kSelThreads) {
+    float4 w[kBatch];
+    int4 p[kBatch];
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        n[b] = 0;
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + 4 * (q + u * kSelThreads);
+      if (a.vec && j + 3 < j1) {
+        w[u] = *reinterpret_cast<const float4*>(weight + j);
+        p[u] = *reinterpret_cast<const int4*>(pos + j);
+      } else {
+        float* wu = reinterpret_cast<float*>(&w[u]);
+        int* pu = reinterpret_cast<int*>(&p[u]);
 #pragma unroll
-        for (int c = 0; c < kHistCopies; ++c) n[b] += hist[c][255 - 8 * tid - b];
-        sum += n[b];
-      }
-      uint32_t inc = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (tid >= d) inc += o;
-      }
-      uint32_t above = inc - sum;
-      if (above < want && want <= inc) {
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          if (above < want && want <= above + n[b]) {
-            found[0] = uint32_t(255 - 8 * tid - b) | (n[b] << 8);
-            found[1] = want - above;
-          }
-          above += n[b];
+        for (int x = 0; x < 4; ++x) {
+          wu[x] = j + x < j1 ? weight[j + x] : 0.f;
+          pu[x] = j + x < j1 ? pos[j + x] : 0;
         }
       }
     }
-    __syncthreads();
-    prefix |= (found[0] & 255u) << shift;
-    equal = found[0] >> 8;
-    mask |= 255u << shift;
-    want = found[1];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int j = j0 + 4 * (q + u * kSelThreads);
+      const float* wu = reinterpret_cast<const float*>(&w[u]);
+      const int* pu = reinterpret_cast<const int*>(&p[u]);
+      if (j >= j1) break;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (j + x < j1) {
+          const uint32_t k = keep_key(wu[x], pu[x], a.sinks, recent_from);
+          if (j + x - j0 < a.smem_keys) keys[j + x - j0] = k;
+          const uint64_t v = packed(k, j + x);
+          low = v < low ? v : low;
+        }
+      }
+      // out of place: the scores below the budget (free places are written over below)
+      if (!a.in_place) {
+        if (a.vec && j + 3 < min(j1, a.budget)) {
+          *reinterpret_cast<float4*>(weight_out + j) = w[u];
+          *reinterpret_cast<int4*>(pos_out + j) = p[u];
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (j + x < min(j1, a.budget)) {
+              weight_out[j + x] = wu[x];
+              pos_out[j + x] = pu[x];
+            }
+        }
+      }
+    }
   }
-  // kept: keys above `prefix`, and the first `want` of the `equal` keys at it
-  const bool some_ties = equal > want;
-  uint32_t ties_before = 0, holes_before = 0, moved_before = 0;
+  if (E <= 0) return;
+
+  if (few) {
+    auto least = [](uint64_t v) {   // over the warp
+      const uint32_t hi = uint32_t(v >> 32), top = __reduce_min_sync(0xffffffffu, hi);
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, hi == top ? uint32_t(v) : 0xFFFFFFFFu);
+      return uint64_t(top) << 32 | lo;
+    };
+    for (int e = 0; e < E; ++e) {
+      const uint64_t mine = least(low);
+      if (lane == 0) lowest[e & 1][warp] = mine;
+      __syncthreads();
+      const uint64_t all = least(lane < kSelWarps ? lowest[e & 1][lane] : ~uint64_t(0));
+      const int j = int(~uint32_t(all));
+      if (tid == 0) dropped[e] = j;
+      if (j / 4 % kSelThreads == tid) {   // the next lowest of the thread that held it (j0 = 0 here)
+        low = ~uint64_t(0);
+        for (int x0 = 4 * tid; x0 < j1; x0 += 4 * kSelThreads)
+          for (int x = x0; x < min(j1, x0 + 4); ++x) {
+            const uint64_t v = packed(key(x), x);
+            if (v > all) low = v < low ? v : low;   // those taken before are all below
+          }
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // places below the budget that fall free, and tokens past it that stay, each in order
+      const int mine = lane < E ? dropped[lane] : -1;
+      const bool hole = lane < E && mine < a.budget;
+      int rank_hole = 0;
+      bool stays = lane < E;
+      for (int e = 0; e < E; ++e) {
+        const int other = __shfl_sync(0xffffffffu, mine, e);
+        if (other < mine) rank_hole += other < a.budget ? 1 : 0;
+        if (other == a.budget + lane) stays = false;
+      }
+      if (hole) few_dst[rank_hole] = mine;
+      const uint32_t stay = __ballot_sync(0xffffffffu, stays);
+      if (stays) few_src[__popc(stay & ((1u << lane) - 1u))] = a.budget + lane;
+      if (lane == 0) found[0] = uint32_t(__popc(stay));
+    }
+    __syncthreads();
+    // a warp a move
+    for (int i = warp; i < int(found[0]); i += kSelWarps) {
+      const int from = few_src[i], to = few_dst[i];
+      const uint32_t ps = page_of(a.c, s, uint32_t(from)), pd = page_of(a.c, s, uint32_t(to));
+      if (ps < a.c.n_pages && pd < a.c.n_pages) {
+        // lanes 0-15 the K row's sixteen 16-byte pieces, lanes 16-31 the V row's
+        uint8_t* pool = (lane < 16 ? a.c.k : a.c.v) + (lane & 15) * 16;
+        *reinterpret_cast<uint4*>(pool + uint64_t(row_unit(a.c, pd, uint32_t(to), h)) * kRowBytes) =
+            *reinterpret_cast<const uint4*>(pool + uint64_t(row_unit(a.c, ps, uint32_t(from), h)) * kRowBytes);
+      } else {
+        record(a.c, kBadPage);
+      }
+      if (lane == 0) weight_out[to] = weight[from];   // from >= budget > to
+      if (lane == 1) pos_out[to] = pos[from];
+    }
+    return;
+  }
+
+  // ---- radix selection ----
+  uint32_t prefix = 0, mask = 0, want = uint32_t(a.budget);   // rank, from the top, among keys that share `prefix`
+  uint32_t equal = 0;
+  constexpr int kShift[3] = {21, 10, 0}, kWidth[3] = {11, 11, 10};
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = kShift[pass];
+    const uint32_t n_bins = 1u << kWidth[pass];
+    for (uint32_t i = tid; i < n_bins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int jb = j0 + warp * 32; jb < j1; jb += kSelThreads) {   // whole warps
+      const int j = jb + lane;
+      const uint32_t k = j < j1 ? key(j) : 0u;
+      const bool on = j < j1 && (k & mask) == prefix;
+      const uint32_t bin = (k >> shift) & (n_bins - 1u);
+      // the first lane's bin is counted by one addition for all that share it
+      // (runs of protected tokens or of zeros), the others one by one
+      const uint32_t act = __ballot_sync(0xffffffffu, on);
+      if (act) {
+        const int lead = __ffs(act) - 1;
+        const uint32_t bin0 = __shfl_sync(0xffffffffu, bin, lead);
+        const uint32_t same = __ballot_sync(0xffffffffu, on && bin == bin0);
+        if (lane == lead) atomicAdd(&hist[bin0], uint32_t(__popc(same)));
+        else if (on && bin != bin0) atomicAdd(&hist[bin], 1u);
+      }
+    }
+    __syncthreads();
+    if (cs > 1) {
+      // every block adds its bins to every block's sums
+      if (pass == 0) ptx::cluster_wait();
+      for (uint32_t i = tid; i < n_bins; i += kSelThreads) {
+        const uint32_t n = hist[i];
+        if (n == 0) continue;
+        const uint32_t at = ptx::smem_u32(&bins[pass][i]);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < cs) ptx::red_add_cluster(ptx::mapa_shared(at, uint32_t(r)), n);
+      }
+      sync();
+    }
+    // bins from the top, four (two in the last pass) a thread
+    const uint32_t* all = cs > 1 ? bins[pass] : hist;
+    const uint32_t per = n_bins / kSelThreads, top = n_bins - 1u - uint32_t(tid) * per;
+    uint32_t sum = 0;
+    for (uint32_t b = 0; b < per; ++b) sum += all[top - b];
+    const uint32_t inc = warp_scan(sum);
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    uint32_t above = inc - sum;
+    for (int w = 0; w < warp; ++w) above += warp_sums[w];
+    if (above < want && want <= above + sum) {
+      for (uint32_t b = 0; b < per; ++b) {
+        const uint32_t n = all[top - b];
+        if (above < want && want <= above + n) {
+          found[0] = top - b;
+          found[1] = want - above;
+          found[2] = n;
+        }
+        above += n;
+      }
+    }
+    __syncthreads();
+    prefix |= found[0] << shift;
+    mask |= (n_bins - 1u) << shift;
+    want = found[1];
+    equal = found[2];
+  }
+
+  // kept: keys above `prefix`, and the first `want` of the `equal` keys at it.
+  // Warp w of block r goes over the w-th part of the block's tokens: it counts
+  // ties, then free places and moves, and writes them from where the warps and
+  // blocks before it end.
+  const int part = (seg / 32 + kSelWarps - 1) / kSelWarps * 32;
+  const int wj0 = min(j1, j0 + warp * part), wj1 = min(j1, wj0 + part);
+  // exclusive prefix of a warp's count over the warps and blocks before it, and the sum of all
+  auto prefix_of = [&](uint32_t mine, int slot, uint32_t& sum) {
+    __syncthreads();   // warp_sums of an earlier use are read
+    if (lane == 0) warp_sums[warp] = mine;
+    __syncthreads();
+    uint32_t before = 0, block = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      before += w < warp ? warp_sums[w] : 0u;
+      block += warp_sums[w];
+    }
+    sum = block;
+    if (cs > 1) {
+      if (tid < cs) ptx::st_cluster(ptx::mapa_shared(ptx::smem_u32(&block_sums[slot][rank]), uint32_t(tid)), block);
+      sync();
+      sum = 0;
+      for (int r = 0; r < cs; ++r) {
+        before += r < rank ? block_sums[slot][r] : 0u;
+        sum += block_sums[slot][r];
+      }
+    }
+    return before;
+  };
+  uint32_t ties_before = 0;
+  if (equal > want) {
+    uint32_t n = 0, sum;
+    for (int jb = wj0; jb < wj1; jb += 32)
+      n += uint32_t(__popc(__ballot_sync(0xffffffffu, jb + lane < wj1 && key(jb + lane) == prefix)));
+    ties_before = prefix_of(n, 2, sum);
+  }
+  // which of a warp's 32 tokens from jb on are kept
+  auto kept = [&](int jb, uint32_t& ties) {
+    const int j = jb + lane;
+    const uint32_t k = j < wj1 ? key(j) : 0u;
+    bool keep = j < wj1 && k >= prefix;
+    if (equal > want) {
+      const uint32_t tie = __ballot_sync(0xffffffffu, j < wj1 && k == prefix);
+      if (j < wj1 && k == prefix && ties + __popc(tie & ((1u << lane) - 1u)) >= want) keep = false;
+      ties += uint32_t(__popc(tie));
+    }
+    return keep;
+  };
+  uint32_t ties = ties_before, holes = 0, moved = 0;
+  for (int jb = wj0; jb < wj1; jb += 32) {
+    const bool keep = kept(jb, ties);
+    const int j = jb + lane;
+    holes += uint32_t(__popc(__ballot_sync(0xffffffffu, j < wj1 && j < a.budget && !keep)));
+    moved += uint32_t(__popc(__ballot_sync(0xffffffffu, j >= a.budget && keep)));
+  }
+  // two counts of a head, each below 2^30: one after the other
+  uint32_t total = 0;
+  uint32_t hole_at = prefix_of(holes, 0, total);
+  uint32_t move_at = prefix_of(moved, 1, total);
   int32_t* src = a.src + int64_t(item) * a.max_moves;
   int32_t* dst = a.dst + int64_t(item) * a.max_moves;
-  for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t k = j < L ? key(j) : 0u;
-    const bool tie = j < L && k == prefix;
-    bool keep = j < L && k >= prefix;
-    if (some_ties) {
-      uint32_t total;
-      const uint32_t rank = ties_before + block_scan(tie ? 1u : 0u, warp_sums, total);
-      if (tie && rank >= want) keep = false;
-      ties_before += total;
-    }
-    const bool hole = j < a.budget && j < L && !keep, moved = j >= a.budget && keep;
-    uint32_t total;
-    const uint32_t at = block_scan((hole ? 1u : 0u) | (moved ? 0x10000u : 0u), warp_sums, total);
-    if (hole) dst[holes_before + (at & 0xFFFFu)] = j;
-    if (moved) src[moved_before + (at >> 16)] = j;
-    if (!a.in_place && keep && j < a.budget) {
-      weight_out[j] = weight[j];
-      pos_out[j] = pos[j];
-    }
-    holes_before += total & 0xFFFFu;
-    moved_before += total >> 16;
+  ties = ties_before;
+  for (int jb = wj0; jb < wj1; jb += 32) {
+    const bool keep = kept(jb, ties);
+    const int j = jb + lane;
+    const bool hole = j < wj1 && j < a.budget && !keep, move = j >= a.budget && keep;
+    const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, move);
+    if (hole) dst[hole_at + __popc(hb & ((1u << lane) - 1u))] = j;
+    if (move) src[move_at + __popc(mb & ((1u << lane) - 1u))] = j;
+    hole_at += uint32_t(__popc(hb));
+    move_at += uint32_t(__popc(mb));
   }
-  __syncthreads();   // the block's lists are written
-  if (tid == 0) a.count[item] = int(moved_before);
-  for (int t = tid; t < int(moved_before); t += kSelThreads) {
-    const int from = src[t], to = dst[t];
+  sync();   // the head's lists are written, and the kept scores
+  if (tid == 0 && rank == 0) a.count[item] = int(total);
+  for (int i = rank * kSelThreads + tid; i < int(total); i += cs * kSelThreads) {
+    const int from = src[i], to = dst[i];
     weight_out[to] = weight[from];   // from >= budget > to: no index is both read and written
     pos_out[to] = pos[from];
+    // the second launch gets the rows themselves (equal ones: nothing to move)
+    const uint32_t ps = page_of(a.c, s, uint32_t(from)), pd = page_of(a.c, s, uint32_t(to));
+    const bool ok = ps < a.c.n_pages && pd < a.c.n_pages;
+    if (!ok) record(a.c, kBadPage);
+    src[i] = ok ? int32_t(row_unit(a.c, ps, uint32_t(from), h)) : 0;
+    dst[i] = ok ? int32_t(row_unit(a.c, pd, uint32_t(to), h)) : 0;
   }
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 4;
+constexpr int kMoveUnroll = 8;
 
-// The K and V rows of the moves: a warp takes kMoveUnroll moves at a time,
-// lanes 0-15 the K row's sixteen 16-byte pieces, lanes 16-31 the V row's.
+// The K and V rows of the moves the selection left, a warp kMoveUnroll rows at
+// a time; and the new lengths, where they are in the place of the old.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   const int item = int(blockIdx.x) / a.blocks_per_item, part = int(blockIdx.x) - item * a.blocks_per_item;
   const int s = item / a.c.H, h = item - s * a.c.H;
   ptx::pdl_wait();
-  if (part == 0 && h == 0 && threadIdx.x == 0) {
+  ptx::pdl_launch_dependents();
+  if (!a.lens_here && part == 0 && h == 0 && threadIdx.x == 0) {
     const int L = seq_len(a.c, a.seq_lens, s);
     a.seq_lens_out[s] = min(L, a.budget);
   }
@@ -328,29 +545,23 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* src = a.src + int64_t(item) * a.max_moves;
   const int32_t* dst = a.dst + int64_t(item) * a.max_moves;
+  // lanes 0-15 the K row's sixteen 16-byte pieces, lanes 16-31 the V row's
   uint8_t* pool = (lane < 16 ? a.c.k : a.c.v) + (lane & 15) * 16;
-  for (int t0 = (part * (kMoveThreads / 32) + warp) * kMoveUnroll; t0 < n;
-       t0 += a.blocks_per_item * (kMoveThreads / 32) * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    uint32_t to[kMoveUnroll];
-    bool ok[kMoveUnroll];
+  for (int t0 = (part * (kMoveThreads / 32) + warp) * 32; t0 < n; t0 += a.blocks_per_item * kMoveThreads) {
+    const bool there = t0 + lane < n;
+    const uint32_t from = there ? uint32_t(src[t0 + lane]) : 0u, to = there ? uint32_t(dst[t0 + lane]) : 0u;
+#pragma unroll 1
+    for (int u0 = 0; u0 < 32 && t0 + u0 < n; u0 += kMoveUnroll) {
+      uint4 x[kMoveUnroll];
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      ok[u] = t0 + u < n;
-      if (!ok[u]) continue;
-      const uint32_t js = uint32_t(src[t0 + u]), jd = uint32_t(dst[t0 + u]);
-      const uint32_t ps = page_of(a.c, s, js), pd = page_of(a.c, s, jd);
-      ok[u] = ps < a.c.n_pages && pd < a.c.n_pages;
-      if (!ok[u]) {
-        record(a.c, kBadPage);
-        continue;
+      for (int u = 0; u < kMoveUnroll; ++u)
+        x[u] = *reinterpret_cast<const uint4*>(pool + uint64_t(__shfl_sync(0xffffffffu, from, u0 + u)) * kRowBytes);
+#pragma unroll
+      for (int u = 0; u < kMoveUnroll; ++u) {
+        const uint32_t f = __shfl_sync(0xffffffffu, from, u0 + u), d = __shfl_sync(0xffffffffu, to, u0 + u);
+        if (f != d) *reinterpret_cast<uint4*>(pool + uint64_t(d) * kRowBytes) = x[u];
       }
-      x[u] = *reinterpret_cast<const uint4*>(pool + uint64_t(row_unit(a.c, ps, js, h)) * kRowBytes);
-      to[u] = row_unit(a.c, pd, jd, h);
     }
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (ok[u]) *reinterpret_cast<uint4*>(pool + uint64_t(to[u]) * kRowBytes) = x[u];
   }
 }
 
@@ -405,8 +616,8 @@ extern "C" rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const v
   a.div_new = make_fastdiv(uint32_t(n_new));
   a.total = uint32_t(pieces);
   const uint32_t per = kInsertThreads * kInsertUnroll;
-  paged_insert_kernel<<<(a.total + per - 1) / per, kInsertThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_overlapped(paged_insert_kernel, dim3((a.total + per - 1) / per), kInsertThreads, 0,
+                                          static_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return cuda_fail(e, "paged_insert_kernel launch");
   return RKV_OK;
 }
@@ -432,7 +643,11 @@ extern "C" rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const in
     return fail(RKV_ERR_INVALID_ARG, "seq_lens/weight/pos/next_pos or an output is NULL");
   if (budget < 1) return fail(RKV_ERR_INVALID_ARG, "budget must be >= 1");
   if (sinks < 0 || recent < 0) return fail(RKV_ERR_INVALID_ARG, "sinks and recent must be >= 0");
-  const uint64_t sb = score_bytes(cache);
+  const uint64_t sb = score_bytes(cache), lb = uint64_t(cache->n_seqs) * 4;
+  if ((seq_lens_out != seq_lens && overlaps(seq_lens_out, lb, seq_lens, lb)) || overlaps(seq_lens_out, lb, next_pos, lb) ||
+      overlaps(seq_lens_out, lb, weight, sb) || overlaps(seq_lens_out, lb, pos, sb) ||
+      overlaps(seq_lens_out, lb, weight_out, sb) || overlaps(seq_lens_out, lb, pos_out, sb))
+    return fail(RKV_ERR_INVALID_ARG, "seq_lens_out overlaps an input or another output");
   const bool in_place = weight_out == weight;
   if (in_place != (pos_out == pos)) return fail(RKV_ERR_INVALID_ARG, "weight_out and pos_out are in place both or neither");
   if (overlaps(weight, sb, pos, sb) || overlaps(weight_out, sb, pos_out, sb) ||
@@ -460,34 +675,34 @@ extern "C" rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const in
   a.recent = recent;
   a.in_place = in_place ? 1 : 0;
   a.max_moves = int32_t(max_moves(cache, budget));
+  a.vec = capacity(cache) % 4 == 0 && aligned16(weight) && aligned16(pos) && aligned16(weight_out) && aligned16(pos_out);
   a.count = static_cast<int32_t*>(workspace);
   a.src = a.count + items;
   a.dst = a.src + items * a.max_moves;
+  a.lens_here = seq_lens_out != seq_lens;
+  // blocks a head: one where the heads and sequences alone fill the machine
+  // (or a head is short), else up to eight
+  const int sms = sm_count();
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && items * a.cluster * 2 <= 2 * sms && capacity(cache) >= 2048 * int64_t(a.cluster))
+    a.cluster *= 2;
   constexpr int kMaxSmemKeys = 48 * 1024;
-  a.smem_keys = int32_t(std::min<int64_t>(capacity(cache), kMaxSmemKeys));
-  const int smem = a.smem_keys * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int64_t seg = ((capacity(cache) + a.cluster - 1) / a.cluster + 31) / 32 * 32;
+  a.smem_keys = int32_t(std::min<int64_t>(seg, kMaxSmemKeys));
+  cudaError_t e = allow_smem<evict_select_kernel>(kMaxSmemKeys * 4);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(evict_select_kernel)");
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  evict_select_kernel<<<uint32_t(items), kSelThreads, smem, cs>>>(a);
-  e = cudaGetLastError();
+  e = launch_overlapped(evict_select_kernel, dim3(uint32_t(items * a.cluster)), kSelThreads, size_t(a.smem_keys) * 4, cs,
+                        a, a.cluster);
   if (e != cudaSuccess) return cuda_fail(e, "evict_select_kernel launch");
+  // no second launch where the selection moves every row itself and the new
+  // lengths are apart from the old
+  if (a.cluster == 1 && capacity(cache) - budget <= kFew && a.lens_here) return RKV_OK;
   // enough blocks to fill the machine about twice over, no more than the moves need
-  const int64_t per = (kMoveThreads / 32) * kMoveUnroll;
-  const int64_t most = std::max<int64_t>(1, (a.max_moves + per - 1) / per);
-  const int64_t want = (int64_t(sm_count()) * 16 + items - 1) / items;
+  const int64_t most = std::max<int64_t>(1, (a.max_moves + kMoveThreads - 1) / kMoveThreads);
+  const int64_t want = (int64_t(sms) * 16 + items - 1) / items;
   a.blocks_per_item = int32_t(std::min(most, std::max<int64_t>(1, want)));
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(uint32_t(items * a.blocks_per_item));
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = cs;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_move_kernel, a);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  e = launch_overlapped(evict_move_kernel, dim3(uint32_t(items * a.blocks_per_item)), kMoveThreads, 0, cs, a);
   if (e != cudaSuccess) return cuda_fail(e, "evict_move_kernel launch");
   return RKV_OK;
 }

@@ -3,6 +3,8 @@
 // and the host checks of an rkv_paged_cache.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace rkv {
@@ -59,6 +61,44 @@ CacheDev cache_dev(const rkv_paged_cache* c);   // of a checked cache
 // Does [p, p + bytes) share a byte with a page of the pool?
 bool overlaps_pool(const rkv_paged_cache* c, const void* p, uint64_t bytes);
 int sm_count();
+
+// Allow kernel kKern `bytes` of dynamic shared memory on the current device:
+// once per device, since the call takes as long as a small launch.
+template <auto kKern>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};   // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Launch that may overlap the end of the stream's previous launch (the kernel
+// waits for it before it reads anything), as clusters of `cluster` blocks.
+template <class Args>
+inline cudaError_t launch_overlapped(void (*kern)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                     const Args& args, int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = uint32_t(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(uint32_t(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
 
 inline int64_t capacity(const rkv_paged_cache* c) { return int64_t(c->max_pages) * c->page_tokens; }
 

@@ -489,6 +489,12 @@ def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, str
         raise ValueError("need at least one sequence")
     if len(windows) != len(seqs):
         raise ValueError("need one (window_blocks, sink_blocks) per sequence")
+    index = seqs[0].q.get_device()
+    if any(x.get_device() != index for s in seqs for x in (s.q, s.k, s.v, s.o)):
+        raise ValueError("the sequences of one launch must be on one device")
+    if index >= 0 and _elsewhere(index, stream):
+        with _on(seqs[0].q, stream):
+            return attn_fwd_window(seqs, windows, rope, softmax_scale, workspace)
     H, D, H_kv = seqs[0].q.shape[1], seqs[0].q.shape[2], seqs[0].k.shape[1]
     for s in seqs:
         if tuple(s.q.shape[1:]) != (H, D) or tuple(s.o.shape[1:]) != (H, D) or tuple(s.k.shape[1:]) != (H_kv, D) \
@@ -498,12 +504,11 @@ def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, str
     win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(int(w), int(k)) for w, k in windows])
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
-    with _on(seqs[0].q, stream) as st:
-        if workspace is None:
-            workspace = torch.empty(attn_fwd_varlen_workspace_size(len(seqs), H, D), dtype=torch.uint8,
-                                    device=seqs[0].q.device)
-        _check(_lib.attn_fwd_window(arr, win, len(seqs), H, H_kv, D, float(softmax_scale), ctypes.byref(rope),
-                                    workspace.data_ptr(), workspace.numel(), st))
+    if workspace is None:
+        workspace = torch.empty(attn_fwd_varlen_workspace_size(len(seqs), H, D), dtype=torch.uint8,
+                                device=seqs[0].q.device)
+    _check(_lib.attn_fwd_window(arr, win, len(seqs), H, H_kv, D, float(softmax_scale), ctypes.byref(rope),
+                                workspace.data_ptr(), workspace.nbytes, _raw_stream(index)))
     return workspace
 
 
@@ -531,35 +536,45 @@ def attn_window_rows(seqs, windows, H, rope):
 
 
 class _on:
-    """Stream handle of a call on tensors of t's device: the given stream, or
-    the device's current one.  Inside, that device and stream are current, so
-    what the call allocates belongs to the stream it runs on."""
-
-    __slots__ = ("guards", "device", "stream")
+    """Makes t's device current for a call on a stream that is not its current
+    one, and that stream too, so that what the call allocates belongs to the
+    stream it runs on."""
 
     def __init__(self, t, stream):
-        self.device, self.stream, self.guards = t.device, stream, []
+        import torch
+        if stream is not None and stream.device != t.device:
+            raise ValueError("the stream and the tensors are on different devices")
+        self.guard = torch.cuda.device(t.device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        import torch
-        if self.device.type != "cuda":
-            return ctypes.c_void_p(0)   # nothing runs: the library refuses host tensors' work
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError("the stream and the tensors are on different devices")
-            g = torch.cuda.stream(self.stream)      # makes the stream's device current too
-        elif self.device.index != torch.cuda.current_device():
-            g = torch.cuda.device(self.device)
-        else:
-            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(self.device.index))
-        g.__enter__()
-        self.guards.append(g)
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        self.guard.__enter__()
 
     def __exit__(self, *exc):
-        while self.guards:
-            self.guards.pop().__exit__(*exc)
-        return False
+        return self.guard.__exit__(*exc)
+
+
+def _elsewhere(index, stream):
+    """Whether a call on tensors of device ``index`` has to be made under _on."""
+    import torch
+    return stream is not None or torch._C._cuda_getDevice() != index
+
+
+def _raw_stream(index):
+    """Handle of the current stream of device ``index``."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _row_stride(t, name, shape, index):
+    """Row stride of a bf16 tensor [L, H, D] of the given shape on device
+    ``index`` whose rows are contiguous."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(shape)} on the cache's device")
+    s = t.stride()
+    if s[2] != 1 or s[1] != shape[2]:
+        raise ValueError(f"{name}: each row must hold H*D contiguous values")
+    return s[0]
 
 
 class PagedKVCache:
@@ -584,7 +599,9 @@ class PagedKVCache:
         self.k, self.v, self.page_table = k, v, page_table
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.n_seqs, self.max_pages = page_table.shape
-        self.H, self.capacity = H, self.max_pages * P
+        self.H, self.capacity, self.index = H, self.max_pages * P, k.get_device()
+        self._per_seq = torch.Size((self.n_seqs,))
+        self._per_token = torch.Size((self.n_seqs, H, self.capacity))
         # a single page's or sequence's stride says nothing: any will do
         stride = k.stride(0) if n_pages > 1 else P * H * D
         table_stride = page_table.stride(0) if self.n_seqs > 1 else self.max_pages
@@ -595,8 +612,8 @@ class PagedKVCache:
     def _ints(self, t, name):
         """Device pointer of an int32 [n_seqs] tensor."""
         import torch
-        if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != self.n_seqs or not t.is_contiguous() \
-                or t.device != self.k.device:
+        if t.dtype is not torch.int32 or t.shape != self._per_seq or t.get_device() != self.index \
+                or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 [n_seqs={self.n_seqs}] tensor on the cache's device")
         return t.data_ptr()
 
@@ -604,19 +621,20 @@ class PagedKVCache:
         """Device pointer of a [n_seqs, H, capacity] tensor, or NULL for None."""
         if t is None:
             return None
-        if t.dtype != dtype or t.shape != (self.n_seqs, self.H, self.capacity) or not t.is_contiguous() \
-                or t.device != self.k.device:
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
-                             f"{(self.n_seqs, self.H, self.capacity)} on the cache's device")
+        if t.dtype is not dtype or t.shape != self._per_token or t.get_device() != self.index \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(self._per_token)} on the "
+                             "cache's device")
         return t.data_ptr()
 
     def _workspace(self, t, size):
+        """A workspace tensor, allocated here when None, and its bytes."""
         import torch
         if t is None:
-            return torch.empty(max(16, size), dtype=torch.uint8, device=self.k.device)
-        if t.device != self.k.device or not t.is_contiguous():
+            t = torch.empty(max(16, size), dtype=torch.uint8, device=self.k.device)
+        elif t.get_device() != self.index or not t.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        return t
+        return t, t.nbytes
 
 
 def kvcache_paged_insert(cache, k_new, v_new, seq_lens, next_pos=None, pos=None, weight=None, stream=None):
@@ -625,20 +643,20 @@ def kvcache_paged_insert(cache, k_new, v_new, seq_lens, next_pos=None, pos=None,
     [n_seqs]) counts them already.  ``pos`` (with ``next_pos``) and ``weight``:
     the scores of the new tokens (see rkv.h)."""
     import torch
-    ks, vs = _rows(k_new, "k_new"), _rows(v_new, "v_new")
-    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (cache.H, 128) or k_new.shape[0] % cache.n_seqs:
-        raise ValueError(f"k_new and v_new must be [n_seqs * n_new, {cache.H}, 128]")
-    if ks != vs:
+    if _elsewhere(cache.index, stream):
+        with _on(cache.k, stream):
+            return kvcache_paged_insert(cache, k_new, v_new, seq_lens, next_pos, pos, weight)
+    shape = k_new.shape
+    if len(shape) != 3 or shape[1] != cache.H or shape[2] != 128 or shape[0] % cache.n_seqs:
+        raise ValueError(f"k_new and v_new must be [n_seqs * n_new, {cache.H}, 128] with n_seqs = {cache.n_seqs}")
+    ks = _row_stride(k_new, "k_new", shape, cache.index)
+    if ks != _row_stride(v_new, "v_new", shape, cache.index):
         raise ValueError("k_new and v_new must share a row stride")
-    if k_new.device != cache.k.device or v_new.device != cache.k.device:
-        raise ValueError("k_new and v_new must be on the cache's device")
-    n_new = k_new.shape[0] // cache.n_seqs
-    with _on(cache.k, stream) as st:
-        _check(_lib.kvcache_paged_insert(cache.ref, k_new.data_ptr(), v_new.data_ptr(), ks, n_new,
-                                         cache._ints(seq_lens, "seq_lens"),
-                                         None if next_pos is None else cache._ints(next_pos, "next_pos"),
-                                         cache._scores(pos, "pos", torch.int32),
-                                         cache._scores(weight, "weight", torch.float32), st))
+    _check(_lib.kvcache_paged_insert(cache.ref, k_new.data_ptr(), v_new.data_ptr(), ks, shape[0] // cache.n_seqs,
+                                     cache._ints(seq_lens, "seq_lens"),
+                                     None if next_pos is None else cache._ints(next_pos, "next_pos"),
+                                     cache._scores(pos, "pos", torch.int32),
+                                     cache._scores(weight, "weight", torch.float32), _raw_stream(cache.index)))
 
 
 def attn_decode_paged_workspace_size(cache, Hq, Lq=1, weights=False):
@@ -654,27 +672,30 @@ def attn_decode_paged(q, cache, seq_lens, o=None, window=0, sinks=0, softmax_sca
     attention weight each cached token received (may be the same tensor).
     Returns o (allocated here when None)."""
     import torch
-    qs = _rows(q, "q")
-    if q.shape[0] % cache.n_seqs or q.device != cache.k.device:
-        raise ValueError(f"q must be [n_seqs * Lq, Hq, 128] with n_seqs = {cache.n_seqs}, on the cache's device")
-    Lq, Hq, D = q.shape[0] // cache.n_seqs, q.shape[1], q.shape[2]
-    if D != 128:
-        raise ValueError("head_dim must be 128")
-    with _on(cache.k, stream) as st:
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os_ = _rows(o, "o")
-        if o.shape != q.shape or o.device != q.device:
-            raise ValueError("o and q must share shape and device")
-        size = 0 if workspace is not None else attn_decode_paged_workspace_size(cache, Hq, Lq, weight_out is not None)
-        workspace = cache._workspace(workspace, size)
-        _check(_lib.attn_decode_paged(cache.ref, q.data_ptr(), o.data_ptr(), qs, os_, Hq, Lq,
-                                      cache._ints(seq_lens, "seq_lens"),
-                                      1.0 / math.sqrt(D) if softmax_scale is None else float(softmax_scale),
-                                      int(window), int(sinks), cache._scores(weight_in, "weight_in", torch.float32),
-                                      cache._scores(weight_out, "weight_out", torch.float32), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), st))
+    if _elsewhere(cache.index, stream):
+        with _on(cache.k, stream):
+            return attn_decode_paged(q, cache, seq_lens, o, window, sinks, softmax_scale, weight_in, weight_out,
+                                     workspace)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != 128 or shape[0] % cache.n_seqs:
+        raise ValueError(f"q must be [n_seqs * Lq, Hq, 128] with n_seqs = {cache.n_seqs}")
+    qs = _row_stride(q, "q", shape, cache.index)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    os_ = _row_stride(o, "o", shape, cache.index)
+    Lq, Hq = shape[0] // cache.n_seqs, shape[1]
+    size = 0 if workspace is not None else attn_decode_paged_workspace_size(cache, Hq, Lq, weight_out is not None)
+    workspace, size = cache._workspace(workspace, size)
+    _check(_lib.attn_decode_paged(cache.ref, q.data_ptr(), o.data_ptr(), qs, os_, Hq, Lq,
+                                  cache._ints(seq_lens, "seq_lens"),
+                                  _SCALE if softmax_scale is None else softmax_scale, window, sinks,
+                                  cache._scores(weight_in, "weight_in", torch.float32),
+                                  cache._scores(weight_out, "weight_out", torch.float32), workspace.data_ptr(), size,
+                                  _raw_stream(cache.index)))
     return o
+
+
+_SCALE = 1.0 / math.sqrt(128)
 
 
 def kvcache_paged_evict_workspace_size(cache, budget):
@@ -687,22 +708,28 @@ def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0,
     the least accumulated weight (see rkv.h).  The outputs default to their
     inputs (in place)."""
     import torch
+    if _elsewhere(cache.index, stream):
+        with _on(cache.k, stream):
+            return kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks, recent, seq_lens_out,
+                                       weight_out, pos_out, workspace)
     if (weight_out is None) != (pos_out is None):
         raise ValueError("weight_out and pos_out go together")
-    with _on(cache.k, stream) as st:
-        size = 0 if workspace is not None else kvcache_paged_evict_workspace_size(cache, budget)
-        workspace = cache._workspace(workspace, size)
-        _check(_lib.kvcache_paged_evict(
-            cache.ref, cache._ints(seq_lens, "seq_lens"), cache._scores(weight, "weight", torch.float32),
-            cache._scores(pos, "pos", torch.int32), cache._ints(next_pos, "next_pos"), int(budget), int(sinks),
-            int(recent), cache._ints(seq_lens if seq_lens_out is None else seq_lens_out, "seq_lens_out"),
-            cache._scores(weight if weight_out is None else weight_out, "weight_out", torch.float32),
-            cache._scores(pos if pos_out is None else pos_out, "pos_out", torch.int32), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st))
+    lens_in, w_in = cache._ints(seq_lens, "seq_lens"), cache._scores(weight, "weight", torch.float32)
+    p_in = cache._scores(pos, "pos", torch.int32)
+    size = 0 if workspace is not None else kvcache_paged_evict_workspace_size(cache, budget)
+    workspace, size = cache._workspace(workspace, size)
+    _check(_lib.kvcache_paged_evict(
+        cache.ref, lens_in, w_in, p_in, cache._ints(next_pos, "next_pos"), budget, sinks, recent,
+        lens_in if seq_lens_out is None else cache._ints(seq_lens_out, "seq_lens_out"),
+        w_in if weight_out is None else cache._scores(weight_out, "weight_out", torch.float32),
+        p_in if pos_out is None else cache._scores(pos_out, "pos_out", torch.int32), workspace.data_ptr(), size,
+        _raw_stream(cache.index)))
 
 
 def rkv_paged_status(cache, stream=None):
     """Synchronise and raise RkvError if a call on ``cache`` met a length or a
     page out of range since the last report."""
-    with _on(cache.k, stream) as st:
-        _check(_lib.rkv_paged_status(cache.ref, st))
+    if _elsewhere(cache.index, stream):
+        with _on(cache.k, stream):
+            return rkv_paged_status(cache)
+    _check(_lib.rkv_paged_status(cache.ref, _raw_stream(cache.index)))

@@ -175,6 +175,22 @@ def test_evict_long_streams():
     evict_case([L], 1, 64, 59999, 5, 2 ** 31 - 1, lambda s, n: w, lambda s, n: p, lambda s, n: -(2 ** 31), True)
 
 
+@pytest.mark.parametrize("L,H,n,budget,sinks,recent,ties", [
+    (9000, 1, 1, 4000, 7, 100, 0), (17001, 2, 1, 16999, 0, 0, 0), (17001, 2, 2, 5, 1, 1, 0), (33000, 3, 1, 20000, 500, 9000, 0),
+    (9000, 1, 1, 4000, 7, 100, 3), (33000, 1, 2, 16384, 0, 2000, 2), (8192, 5, 3, 8000, 0, 0, 1),
+])
+def test_evict_few_long_heads(L, H, n, budget, sinks, recent, ties):
+    # few heads of many tokens: each shared out over a cluster of blocks
+    need_gpu()
+    rng = np.random.default_rng(L + ties)
+    w = rng.exponential(size=(n, H, L)).astype(np.float32)
+    if ties:
+        w = np.floor(w * ties)
+    lens = [L - 3 * s for s in range(n)]
+    order = [np.stack([rng.permutation(x) for _ in range(H)]) for x in lens]
+    evict_case(lens, H, 64, budget, sinks, recent, lambda s, x: w[s, :, :x], lambda s, x: order[s], lambda s, x: x, bool(ties))
+
+
 def test_evict_capacity_below_budget():
     need_gpu()
     assert evict_case([30, 5], 2, 16, 4000, 1, 5, lambda s, L: np.ones((2, L)), lambda s, L: np.tile(np.arange(L), (2, 1)),

@@ -278,7 +278,7 @@ def test_python_refusals():
         rkv.attn_decode_paged(q, c, st.lens_dev.cpu())
     with pytest.raises(ValueError, match="weight_out"):
         rkv.attn_decode_paged(q, c, st.lens_dev, weight_out=torch.zeros(1, 2, 31, device="cuda"))
-    with pytest.raises(ValueError, match="o and q"):
+    with pytest.raises(ValueError, match="o must be"):
         rkv.attn_decode_paged(q, c, st.lens_dev, o=torch.empty(2, 2, D, dtype=q.dtype, device="cuda"))
     with pytest.raises(rkv.RkvError, match="workspace"):
         rkv.attn_decode_paged(q, c, st.lens_dev, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

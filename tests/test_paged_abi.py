@@ -132,7 +132,8 @@ def test_decode_too_many_rows(rkv):
     (dict(lens_out=0), "NULL"), (dict(wout=0), "NULL"), (dict(pout=0), "NULL"), (dict(budget=0), "budget"),
     (dict(sinks=-1), "sinks"), (dict(recent=-1), "recent"), (dict(wout=0x710000000), "both or neither"),
     (dict(wout=0x510000010, pout=0x720000000), "overlap"), (dict(wout=0x710000000, pout=0x710000010), "overlap"),
-    (dict(wout=0x100000000, pout=0x720000000), "pool"), (dict(ws=0), "workspace"), (dict(wsb=15), "workspace"),
+    (dict(wout=0x100000000, pout=0x720000000), "pool"), (dict(lens_out=0x500000004), "seq_lens_out"),
+    (dict(lens_out=0x530000000), "seq_lens_out"), (dict(lens_out=0x510000040), "seq_lens_out"), (dict(ws=0), "workspace"), (dict(wsb=15), "workspace"),
 ])
 def test_evict_rejects(rkv, change, frag):
     assert evict(rkv, cache(rkv), **change) == rkv.RKV_ERR_INVALID_ARG
