@@ -387,13 +387,14 @@ rkv_status rkv_attn_noalloc_status(void* stream);
  *   H, H_kv        query heads and key heads, H a multiple of H_kv; query
  *                  head h reads key head h / (H / H_kv).  k and v are
  *                  [Lk][H_kv][D] with row strides >= H_kv * D.
- * Work follows the mask: a 512-row unit reads the key tiles of the sinks and
- * of its rows' windows only.  A query row that sees no key gets zeros.  Keys
+ * Work follows the mask: a unit of 512 query rows (of up to four heads of a
+ * key head) reads the key tiles of the sinks and of its rows' windows only.  A query row that sees no key gets zeros.  Keys
  * that no row of a unit sees never reach its outputs, whatever they hold; a V
  * row that some rows of a unit see and others do not must be finite, because
  * its product with a weight of zero enters the others' sums.
  * Errors: those of attn_fwd_varlen, plus RKV_ERR_INVALID_ARG for NULL windows,
- * block_frames < 1, window_blocks or sink_blocks < 0, H not a multiple of H_kv.
+ * block_frames < 1, window_blocks or sink_blocks < 0, H not a multiple of H_kv,
+ * and RKV_ERR_UNSUPPORTED for a query row in frame 2^31 - 1 or later.
  */
 typedef struct {
   int32_t window_blocks; /* blocks a row sees, its own included; 0 = all      */
@@ -410,14 +411,19 @@ rkv_status attn_fwd_window(const rkv_attn_seq* seqs, const rkv_attn_window* wind
  * rkv_attn_mask_rows; needs no GPU).  Query row r sees the keys
  * [0, row_sink[r]) and [row_begin[r], row_limit[r]).
  *
- *   seqs, windows, n_seqs, H, rope   as for attn_fwd_window; only Lq, Lk,
- *                  q_frame_offset, block_frames and the frame grid are read
+ *   seqs, windows, n_seqs, H, H_kv, rope   as for attn_fwd_window; only Lq,
+ *                  Lk, q_frame_offset, block_frames and the frame grid are read
  *   row_sink, row_begin, row_limit   host int64 [sum of Lq] each, rows of the
  *                  sequences one after another in the order given
- *   unit_tiles, n_units   as for rkv_attn_mask_rows
+ *   unit_tiles     optional host int32, 4 per work unit: sequence index in the
+ *                  order given, first query head, first query row, key tiles of
+ *                  128 keys.  A unit is 512 / pack rows of `pack` heads of one
+ *                  key head, pack = 4, 2 or 1, the largest that divides H / H_kv
+ *   n_units        optional out: number of work units, at most
+ *                  sum of H * ceil(Lq / 512)
  */
 rkv_status rkv_attn_window_rows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
-                                const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
+                                int32_t H_kv, const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
                                 int32_t* unit_tiles, int64_t* n_units);
 
 /*

@@ -103,6 +103,14 @@ constexpr int kOffTab = kOffV + kStages * kVStageBytes;
 constexpr int kOffBar = kOffTab + kMaxTabEntries * kTabEntryBytes;
 constexpr int kBarBytes = 512;
 constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;   // + alignment slack
+// windowed launches: every softmax thread's key bounds and every softmax
+// warp's, kept out of the registers that hold a row of scores
+constexpr int kOffRows = kOffBar + kBarBytes;
+constexpr int kRowBounds = 16;    // limit, lo, sink of a thread's row
+constexpr int kWarpBounds = 32;   // WarpView
+constexpr int kOffViews = kOffRows + 256 * kRowBounds;
+constexpr int kSmemWindow = kOffViews + 8 * kWarpBounds + 1024;
+static_assert(kSmemWindow <= 232448, "shared memory of one block");
 
 // TMEM columns: S of sub-tile b at 128*b, O of sub-tile b at 256 + 128*b
 __host__ __device__ constexpr uint32_t col_s(int b) { return 128u * uint32_t(b); }
@@ -115,7 +123,11 @@ struct SeqDev {
   int64_t o_stride_bytes;
   int32_t Lq, Lk, q_t0, k_t0, q_frame_offset, block_frames;
   uint32_t flags;
-  int32_t window_blocks, sink_blocks;   // attn_fwd_window: 0 blocks = no window
+  // attn_fwd_window: 0 blocks = no window; keys of the sinks (at most Lk);
+  // tokens of a block; division by block_frames
+  int32_t window_blocks, sink_keys;
+  int64_t block_tokens;
+  FastDiv div_block;
   int32_t n_qblocks;
   int32_t unit_begin;
   int64_t stats_row0;   // debug launches: first row of this sequence in row_stats
@@ -126,6 +138,11 @@ struct Params {
   int32_t n_seqs, H;
   int32_t windowed;   // the launch is attn_fwd_window's
   int32_t group;      // query heads to a key head (1 unless windowed)
+  // query heads of one key head that share a unit, 1, 2 or 4: a unit is then
+  // 512 / pack rows of each, and its four 128-row sub-tiles belong to `pack`
+  // heads, so that a window's tiles serve rows that see nearly the same keys
+  int32_t pack;
+  uint16_t split_unit[64];   // windowed: the units that run as two items
   // work items: units [0, n_whole) whole, then each of the remaining
   // n_split units as two items over the first and second half of its key
   // tiles, whose partial results go to part_o / part_ml
@@ -283,7 +300,16 @@ __device__ __forceinline__ int items_of(const Params& p, int cluster, int n_clus
   if (p.use_sched) return int(p.sched_off[cluster + 1]) - int(p.sched_off[cluster]);
   return cluster < p.total_units ? (p.total_units - cluster + n_clusters - 1) / n_clusters : 0;
 }
+constexpr int kHalfItem = 1 << 30;   // windowed: the item is half of a split unit (0x8000 in the schedule)
+template <bool kWindow>
 __device__ __forceinline__ int item_at(const Params& p, int cluster, int n_clusters, int k) {
+  if constexpr (kWindow) {
+    if (p.use_sched) {
+      const int v = int(p.sched[p.sched_off[cluster] + k]);
+      return v & 0x8000 ? kHalfItem | (v & 0x7FFF) : v;
+    }
+    return cluster + k * n_clusters;
+  }
   return p.use_sched ? int(p.sched[p.sched_off[cluster] + k]) : cluster + k * n_clusters;
 }
 
@@ -295,6 +321,7 @@ struct Unit {
   // j of the list is tile j below `ns` and tile j + skip from there on
   int ns, skip;
   int32_t lo, sink, hi;   // keys some row of the unit sees: [0, sink) and [lo, hi)
+  int32_t row0;           // first query row (of each of the unit's heads)
 };
 
 // Keys [0, limit) of the sequence are visible to query row `row`: the whole
@@ -309,20 +336,23 @@ __host__ __device__ __forceinline__ int64_t row_kv_limit(const SeqDev& s, const 
   return lim < s.Lk ? lim : s.Lk;
 }
 
-// Windowed launches: of the keys up to row_kv_limit, a row sees those from
-// row_kv_begin on and the first `row_kv_sink`.
-__host__ __device__ __forceinline__ int64_t row_kv_begin(const SeqDev& s, const Params& p, int row) {
-  if (s.window_blocks <= 0) return 0;
-  const int64_t qf = int64_t(s.q_frame_offset) + row / int64_t(p.F);
-  const int64_t first = qf / s.block_frames - s.window_blocks + 1;
-  if (first <= 0) return 0;
-  const int64_t lo = first * s.block_frames * int64_t(p.F);
-  return lo < s.Lk ? lo : s.Lk;
-}
-__host__ __device__ __forceinline__ int64_t row_kv_sink(const SeqDev& s, const Params& p, int row) {
-  const int64_t lim = row_kv_limit(s, p, row);
-  const int64_t sink = int64_t(s.sink_blocks) * s.block_frames * int64_t(p.F);
-  return sink < lim ? sink : lim;
+// Windowed launches: the keys [0, sink) and [lo, limit) that a row sees.  The
+// host checks that a row's frame stays below 2^31.
+struct RowView {
+  int32_t limit, lo, sink;
+};
+__host__ __device__ __forceinline__ RowView row_view(const SeqDev& s, const Params& p, int row) {
+#ifdef __CUDA_ARCH__
+  const int64_t blk = fdiv(uint32_t(s.q_frame_offset) + fdiv(uint32_t(row), p.div_F), s.div_block);
+#else
+  const int64_t blk = (int64_t(s.q_frame_offset) + row / int64_t(p.F)) / s.block_frames;
+#endif
+  RowView v;
+  const int64_t lim = (blk + 1) * s.block_tokens, lo = (blk - s.window_blocks + 1) * s.block_tokens;
+  v.limit = int32_t(lim < s.Lk ? lim : s.Lk);
+  v.lo = s.window_blocks <= 0 || lo <= 0 ? 0 : int32_t(lo < s.Lk ? lo : s.Lk);
+  v.sink = s.sink_keys < v.limit ? s.sink_keys : v.limit;
+  return v;
 }
 
 // The key tiles of a windowed unit (rows [first, last] of its sequence): those
@@ -330,9 +360,10 @@ __host__ __device__ __forceinline__ int64_t row_kv_sink(const SeqDev& s, const P
 __host__ __device__ __forceinline__ void window_tiles(const SeqDev& s, const Params& p, int first, int last, Unit& r) {
   // limits and begins grow with the row, so the first row's begin and the last
   // row's limit bound the unit
-  r.hi = int32_t(row_kv_limit(s, p, last));
-  r.lo = int32_t(row_kv_begin(s, p, first));
-  r.sink = int32_t(row_kv_sink(s, p, last));
+  const RowView v = row_view(s, p, last);
+  r.hi = v.limit;
+  r.lo = row_view(s, p, first).lo;
+  r.sink = v.sink;
   r.ns = (r.sink + kBN - 1) / kBN;
   int w0 = r.lo / kBN, w1 = r.hi > r.lo ? (r.hi + kBN - 1) / kBN : w0;
   if (r.ns >= w0) {
@@ -364,7 +395,12 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
   Unit r;
   int u = item;
   r.part = -1;
-  if (item >= p.n_whole) {   // half of a split unit
+  if constexpr (kWindow) {
+    if (item & kHalfItem) {
+      r.part = item & ~kHalfItem;
+      u = p.split_unit[r.part >> 1];
+    }
+  } else if (item >= p.n_whole) {   // half of a split unit
     r.part = item - p.n_whole;
     u = p.n_whole + (r.part >> 1);
   }
@@ -377,9 +413,15 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
   const int ord = local - r.head * s.n_qblocks;
   r.qb = s.block_frames > 0 ? (s.n_qblocks - 1 - ord) : ord;
   int last = (r.qb + 1) * kUnitRows - 1;
+  if constexpr (kWindow) {
+    const int rows = kUnitRows / p.pack;
+    r.head *= p.pack;
+    r.row0 = r.qb * rows;
+    last = r.row0 + rows - 1;
+  }
   if (last > s.Lq - 1) last = s.Lq - 1;
   if constexpr (kWindow) {
-    window_tiles(s, p, r.qb * kUnitRows, last, r);
+    window_tiles(s, p, r.row0, last, r);
   } else {
     const int64_t kv = row_kv_limit(s, p, last);
     r.nkt = int((kv + kBN - 1) / kBN);
@@ -391,6 +433,15 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
     else r.kt1 = r.nkt / 2;
   }
   return r;
+}
+
+// Head (beside the unit's first) and first row (beside the unit's) of sub-tile
+// b of CTA `rank` in a windowed launch.
+__host__ __device__ __forceinline__ int sub_head(int pack, int rank, int b) {
+  return pack == 4 ? 2 * rank + b : (pack == 2 ? b : 0);
+}
+__host__ __device__ __forceinline__ int sub_row(int pack, int rank, int b) {
+  return pack == 4 ? 0 : (pack == 2 ? rank * kBM : (2 * rank + b) * kBM);
 }
 
 // decode_unit on the host, for either kind of launch.
@@ -620,6 +671,90 @@ __device__ __forceinline__ float exp_store_tile_max(const uint32_t (&sr)[4][32],
   return (a01.x + a01.y) + (a23.x + a23.y);
 }
 
+// Windowed launches: what the 32 rows of a softmax warp see, as bounds that are
+// the same for all of them, so that most tiles are told apart by a few
+// comparisons.
+// (at `at` in shared memory: all_lim, all_lo, all_sink, any_lim, any_lo,
+// any_sink: every row sees [0, all_sink) and [all_lo, all_lim), no row a key
+// outside [0, any_sink) and [any_lo, any_lim)).
+__device__ __forceinline__ void warp_view_store(uint32_t at, int32_t limit, int32_t lo, int32_t sink) {
+  const uint32_t all_lim = uint32_t(__reduce_min_sync(0xffffffffu, limit));
+  const uint32_t all_lo = uint32_t(__reduce_max_sync(0xffffffffu, lo));
+  const uint32_t all_sink = uint32_t(__reduce_min_sync(0xffffffffu, sink));
+  const uint32_t any_lim = uint32_t(__reduce_max_sync(0xffffffffu, limit));
+  const uint32_t any_lo = uint32_t(__reduce_min_sync(0xffffffffu, lo));
+  const uint32_t any_sink = uint32_t(__reduce_max_sync(0xffffffffu, sink));
+  ptx::sts128(at, make_uint4(all_lim, all_lo, all_sink, any_lim));   // every lane the same
+  ptx::sts128(at + 16, make_uint4(any_lo, any_sink, 0u, 0u));
+}
+// Of the tile whose first key is kbase: some row sees only part of it; no row
+// sees any of it.
+__device__ __forceinline__ void warp_view_tile(uint32_t at, int kbase, bool& masked, bool& hidden) {
+  const uint4 x = ptx::lds128(at), y = ptx::lds128(at + 16);
+  const int end = kbase + kBN;
+  masked = !(end <= int(x.x) && (kbase >= int(x.y) || end <= int(x.z)));
+  hidden = kbase >= int(x.w) || (end <= int(y.x) && kbase >= int(y.y));
+}
+
+// Bits [0, n) of a word, n brought into [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+
+// The tile whose first key is kbase, of which one thread's row sees the keys in
+// [0, sink) and [lo, limit) (its bounds at `row` in shared memory): its scores
+// are read from TMEM 32 at a time, twice, so that the path needs few registers
+// beside the row that the unmasked path holds.  A warp's 32 rows cut through
+// one or two of the four chunks; the others take no select.
+__device__ __forceinline__ void window_chunk(uint32_t (&r)[32], uint32_t tS, uint32_t row, int kbase, int ch) {
+  ptx::tmem_ld32(tS + ch * 32, r);
+  const uint4 x = ptx::lds128(row);
+  const int at = kbase + 32 * ch;
+  const uint32_t seen = low_bits(int(x.x) - at) & (~low_bits(int(x.y) - at) | low_bits(int(x.z) - at));
+  ptx::tmem_wait_ld();
+  if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(seen & (1u << i))) r[i] = 0xFF800000u;   // -inf
+  }
+}
+__device__ __forceinline__ float window_tile_max(uint32_t tS, uint32_t row, int kbase) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t r[32];
+    window_chunk(r, tS, row, kbase, ch);
+    float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      m2[0] = max3f(m2[0], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+      m2[1] = max3f(m2[1], __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+    }
+    mx = max3f(mx, m2[0], m2[1]);
+  }
+  return mx;
+}
+// exp_store_tile of such a tile: chunk ch's P takes columns 16 ch .. of S,
+// which chunks up to ch have been read from.
+__device__ __forceinline__ float window_tile_exp(uint32_t tS, uint32_t row, int kbase, float scale_log2, float m_use) {
+  float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t r[32], pk[16];
+    window_chunk(r, tS, row, kbase, ch);
+    float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                                  make_float2(scale_log2, scale_log2), make_float2(-m_use, -m_use));
+      const float2 pp = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));   // exp2(-inf) = 0: hidden keys
+      a2[i & 1] = __fadd2_rn(a2[i & 1], pp);
+      pk[i] = pack_bf16x2(pp.x, pp.y);
+    }
+    ptx::tmem_st16(tS + ch * 16, pk);
+    acc = __fadd2_rn(acc, __fadd2_rn(a2[0], a2[1]));
+  }
+  return acc.x + acc.y;
+}
+
 // K-major operand (rows of 128 bf16 in two 64-column 128B-swizzled halves):
 // 8-row groups 1024 bytes apart; k-step kk starts 32 bytes further inside a
 // half, or in the second half from kk = 4.
@@ -739,15 +874,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const float scale_log2 = p.scale_log2;
     uint32_t g = 0, items = 0;
     for (int k = 0; k < n_items; ++k, ++items) {
-      const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+      const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
       const SeqDev& s = p.seq[un.si];
-      const int qrow = un.qb * kUnitRows + int(rank) * kCtaRows + wg * kBM + 32 * (warp & 3) + lane;
-      const int64_t my_limit = row_kv_limit(s, p, qrow < s.Lq ? qrow : s.Lq - 1);
-      int32_t my_lo = 0, my_sink = 0;   // windowed: the row sees [0, my_sink) and [my_lo, my_limit)
+      const int in_tile = 32 * (warp & 3) + lane;
+      const int qrow = kWindow ? un.row0 + sub_row(p.pack, int(rank), wg) + in_tile
+                               : un.qb * kUnitRows + int(rank) * kCtaRows + wg * kBM + in_tile;
+      const int q_head = kWindow ? un.head + sub_head(p.pack, int(rank), wg) : un.head;
+      int64_t my_limit = 0;
+      if constexpr (!kWindow) my_limit = row_kv_limit(s, p, qrow < s.Lq ? qrow : s.Lq - 1);
       if constexpr (kWindow) {
-        my_lo = int32_t(row_kv_begin(s, p, qrow < s.Lq ? qrow : s.Lq - 1));
-        my_sink = int32_t(row_kv_sink(s, p, qrow < s.Lq ? qrow : s.Lq - 1));
-        if (my_sink >= my_lo) my_lo = 0;
+        RowView v = row_view(s, p, qrow < s.Lq ? qrow : s.Lq - 1);
+        if (v.sink >= v.lo) v.lo = 0;
+        ptx::sts128(sbase + kOffRows + uint32_t(tid) * kRowBounds,
+                    make_uint4(uint32_t(v.limit), uint32_t(v.lo), uint32_t(v.sink), 0u));
+        __syncwarp();   // the last unit's view is no longer read
+        warp_view_store(sbase + kOffViews + uint32_t(warp) * kWarpBounds, v.limit, v.lo, v.sink);
+        __syncwarp();
       }
       float m = -INFINITY, l = 0.f;
       RowStats rs = {0u, 0u, 0u, 0u};
@@ -762,31 +904,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int lim = kbase + kBN > my_limit ? int(my_limit - kbase) : kBN;
         // partial tile for some row of the warp: hide keys at or past each
         // row's limit (the keys of a row's mask are a prefix)
-        bool masked = __any_sync(0xffffffffu, lim < kBN);
-        bool hidden = false;   // windowed: no row of the warp sees a key of the tile
-        int lo = 0, sink = 0;  // windowed: within the tile, [0, sink) and [lo, lim) are visible
-        if constexpr (kWindow) {
-          lo = min(max(my_lo - int(kbase), 0), kBN);
-          sink = min(max(my_sink - int(kbase), 0), kBN);
-          if (sink >= lo) lo = 0;
-          masked = __any_sync(0xffffffffu, lim < kBN || lo > 0);
-          hidden = masked && __all_sync(0xffffffffu, lim <= 0 || (lo >= lim && sink <= 0));
-        }
+        bool masked, hidden = false;
+        if constexpr (!kWindow) masked = __any_sync(0xffffffffu, lim < kBN);
+        else warp_view_tile(sbase + kOffViews + uint32_t(warp) * kWarpBounds, int(kbase), masked, hidden);
         const float m_old = m;
         float m_new, tile_sum;
         bool need;
-        if (kWindow && hidden) {
-          // weights of zero, with neither maximum nor exponentials
-          const uint32_t zero[16] = {};
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) ptx::tmem_st16(tS + ch * 16, zero);
-          m_new = m;
-          tile_sum = 0.f;
-          need = false;
-        } else if (j > un.kt0 && !masked) {
+        if (j > un.kt0 && !masked) {
           if constexpr (kDebug) row_stats_tile(sr, uint32_t(kbase), rs);
           // speculative: exponentials against the running max while the
           // tile max is found; redone (rarely) when the max has to move
+          // (always for a windowed row that has seen nothing so far)
           float mx;
           tile_sum = exp_store_tile_max(sr, tS, scale_log2, m, mx);
           m_new = fmaxf(m, mx * scale_log2);
@@ -795,6 +923,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (need) m = m_new;
             tile_sum = exp_store_tile(sr, tS, scale_log2, m);
           }
+        } else if (kWindow && hidden) {
+          // weights of zero, with neither maximum nor exponentials
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) ptx::tmem_st16(tS + ch * 16, zero);
+          m_new = m;
+          tile_sum = 0.f;
+          need = false;
+        } else if (kWindow && masked) {
+          const uint32_t row = sbase + kOffRows + uint32_t(tid) * kRowBounds;
+          m_new = fmaxf(m, window_tile_max(tS, row, int(kbase)) * scale_log2);
+          need = m_new > m + kRescaleLog2;
+          if (need) m = m_new;
+          tile_sum = window_tile_exp(tS, row, int(kbase), scale_log2, m == -INFINITY ? 0.f : m);
         } else {
           if (masked) {
 #pragma unroll
@@ -802,15 +944,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (ch * 32 + i >= lim) sr[ch][i] = 0xFF800000u;   // -inf
-            if constexpr (kWindow) {
-              if (__any_sync(0xffffffffu, lo > 0)) {
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    if (ch * 32 + i < lo && ch * 32 + i >= sink) sr[ch][i] = 0xFF800000u;
-              }
-            }
           }
           if constexpr (kDebug) row_stats_tile(sr, uint32_t(kbase), rs);
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -826,7 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           const float m_use = (m == -INFINITY) ? 0.f : m;
           tile_sum = exp_store_tile(sr, tS, scale_log2, m_use);
         }
-        if (j > un.kt0 && __any_sync(0xffffffffu, need)) {
+        // (a windowed row that has seen nothing so far has an O of zeros)
+        if (j > un.kt0 && __any_sync(0xffffffffu, need && (!kWindow || m_old != -INFINITY))) {
           // O holds tiles 0..j-1 scaled to the old max; S(j) was committed
           // after PV(j-1), so O is complete; rescale in TMEM (PV(j) is not
           // issued before P_FULL below)
@@ -856,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       ptx::tc_fence_after();
       {
         const float inv = l > 0.f ? 1.0f / l : 0.f;
-        uint8_t* orow = s.o + int64_t(qrow) * s.o_stride_bytes + int64_t(un.head) * (kHD * 2);
+        uint8_t* orow = s.o + int64_t(qrow) * s.o_stride_bytes + int64_t(q_head) * (kHD * 2);
         uint32_t r[4][32];
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) ptx::tmem_ld32(tO + ch * 32, r[ch]);
@@ -916,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const uint32_t qready = lbar(B_QREADY);
     uint32_t it = 0, ul = 0;
     for (int k = 0; k < n_items; ++k, ++ul) {
-      const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+      const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
       const SeqDev& s = p.seq[un.si];
       // Every RoPE warp reaches the named barrier below, whether its own wait
       // succeeded or not, and the barrier's AND takes the stop decision for
@@ -925,7 +1059,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       if (okq && (s.flags & RKV_ROPE_Q)) {
         // thread rt rotates row rt of both Q sub-tiles (all 16 chunks)
         for (int b = 0; b < kSub; ++b) {
-          const int row = un.qb * kUnitRows + int(rank) * kCtaRows + b * kBM + rt;
+          const int row = kWindow ? un.row0 + sub_row(p.pack, int(rank), b) + rt
+                                  : un.qb * kUnitRows + int(rank) * kCtaRows + b * kBM + rt;
           if (row < s.Lq) {
             int pt, ph, pw;
             row_positions(p, row, s.q_t0, pt, ph, pw);
@@ -985,7 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0, ul = 0;
       bool ok = true;
       for (int k = 0; k < n_items; ++k, ++ul) {
-        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         const SeqDev& s = p.seq[un.si];
         const int kv_head = kWindow ? un.head / p.group : un.head;
         if (!wait_phase(c, bar(c, B_QFREE), (ul & 1u) ^ 1u, 6)) { ok = false; break; }
@@ -996,8 +1131,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         ptx::mbar_expect_tx(bar(c, B_QFULL), kSub * kQTileBytes);
         for (int b = 0; b < kSub; ++b)
           for (int h2 = 0; h2 < 2; ++h2)
-            ptx::tma_load_3d(sQ + b * kQTileBytes + h2 * kQHalfBytes, &s.tq, bar(c, B_QFULL), h2 * 64, un.head,
-                             un.qb * kUnitRows + int(rank) * kCtaRows + b * kBM);
+            ptx::tma_load_3d(sQ + b * kQTileBytes + h2 * kQHalfBytes, &s.tq, bar(c, B_QFULL), h2 * 64,
+                             kWindow ? un.head + sub_head(p.pack, int(rank), b) : un.head,
+                             kWindow ? un.row0 + sub_row(p.pack, int(rank), b)
+                                     : un.qb * kUnitRows + int(rank) * kCtaRows + b * kBM);
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
           if (!wait_phase(c, bar(c, B_KFREE + st), (n & 1u) ^ 1u, 7)) { ok = false; break; }
@@ -1016,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k) {
-        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         const SeqDev& s = p.seq[un.si];
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
@@ -1037,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k) {
-        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
           if (!wait_warp(c, bar(c, B_VFULL + st), n & 1u, 17)) { ok = false; break; }
@@ -1059,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k) {
-        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
           if (!wait_phase(c, bar(c, B_VFULL + st), n & 1u, 17)) { ok = false; break; }
@@ -1082,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       uint32_t it = 0, g = 0, ul = 0;
       bool ok = true;
       for (int k = 0; ok && k < n_items; ++k, ++ul) {
-        const Unit un = decode_unit<kWindow>(p, item_at(p, cluster, n_clusters, k));
+        const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         if (!wait_phase_cluster(c, bar(c, B_QREADY), ul & 1u, 9)) { ok = false; break; }
         const int nk = un.kt1 - un.kt0;   // tiles of this item; j counts them from 0
         for (int j = 0; j < nk; ++j, ++it, ++g) {
@@ -1229,6 +1366,7 @@ struct CombineArgs {
   const float* part_o;
   const float2* part_ml;
   int32_t n_split;
+  int32_t pack;   // Params::pack
   CombineUnit unit[kMaxSplit];
 };
 
@@ -1241,7 +1379,8 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   const int rem = int(idx - int64_t(u) * kUnitRows * (kHD / 8));
   const int row = rem / (kHD / 8), cg = rem % (kHD / 8);
   const CombineUnit& cu = a.unit[u];
-  const int qrow = cu.row0 + row;
+  const int sub = row / kBM, rank = sub >> 1, b = sub & 1;
+  const int qrow = cu.row0 + sub_row(a.pack, rank, b) + (row - sub * kBM), head = cu.head + sub_head(a.pack, rank, b);
   if (qrow >= cu.Lq) return;
   const int64_t ra = int64_t(2 * u) * kUnitRows + row, rb = ra + kUnitRows;
   const float2 mla = a.part_ml[ra], mlb = a.part_ml[rb];
@@ -1259,7 +1398,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   out.y = pack_bf16x2(a0.z * ca + b0.z * cb, a0.w * ca + b0.w * cb);
   out.z = pack_bf16x2(a1.x * ca + b1.x * cb, a1.y * ca + b1.y * cb);
   out.w = pack_bf16x2(a1.z * ca + b1.z * cb, a1.w * ca + b1.w * cb);
-  *reinterpret_cast<uint4*>(cu.o + int64_t(qrow) * cu.o_stride_bytes + int64_t(cu.head) * (kHD * 2) + cg * 16) = out;
+  *reinterpret_cast<uint4*>(cu.o + int64_t(qrow) * cu.o_stride_bytes + int64_t(head) * (kHD * 2) + cg * 16) = out;
 }
 
 // Launch shape of the attention kernel (attributes set, cluster of 2) and the
@@ -1283,7 +1422,8 @@ static rkv_status attn_launch_shape(const KernelKind& kind, cudaLaunchConfig_t& 
                                     const void*& kern_ptr, int& max_clusters) {
   auto kern = attn_kernel_for(kind);
   kern_ptr = reinterpret_cast<const void*>(kern);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const int smem = kind.windowed ? kSmemWindow : kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attn_fwd_kernel)");
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cluster size)");
@@ -1292,7 +1432,7 @@ static rkv_status attn_launch_shape(const KernelKind& kind, cudaLaunchConfig_t& 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2 * 74);
@@ -1351,6 +1491,79 @@ static bool build_schedule(Params& p, int64_t units, int max_clusters) {
   return true;
 }
 
+// Windowed launches: units differ in cost, and there may be few of them.  The
+// longest-first assignment above, with some of the longest units run as two
+// items (halves of their key tiles, merged by attn_combine_kernel) where that
+// shortens the busiest pair's work.  Fills p.use_sched, p.sched_off, p.sched
+// and p.split_unit; returns the number of split units.
+static int build_window_schedule(Params& p, int64_t units, int max_clusters, int max_split) {
+  p.use_sched = 0;
+  if (units + kMaxSplit > kMaxSched || max_clusters > kMaxClusters) return 0;
+  struct Item {
+    int32_t cost;
+    uint16_t code;
+  };
+  const int n = int(units);
+  std::vector<Item> whole(static_cast<size_t>(n));
+  for (int u = 0; u < n; ++u) whole[size_t(u)] = {host_unit(p, u).nkt, uint16_t(u)};
+  std::stable_sort(whole.begin(), whole.end(), [](const Item& a, const Item& b) { return a.cost > b.cost; });
+  int most = 0;   // units long enough to be halved
+  while (most < std::min(n, max_split) && whole[size_t(most)].cost >= 4) ++most;
+  // Work of the busiest pair, in key tiles, when the first k units are halved;
+  // an item costs kUnitOverheadTiles beside its tiles, the merge about two
+  std::vector<Item> items;
+  std::vector<std::pair<int32_t, int32_t>> heap;   // (work, pair), smallest on top
+  std::vector<std::vector<uint16_t>> lists;
+  auto assign = [&](int k, bool keep) {
+    items.clear();
+    for (int i = 0; i < n; ++i) {
+      if (i < k) {
+        const int half = whole[size_t(i)].cost / 2;
+        items.push_back({half, uint16_t(0x8000 | (2 * i))});
+        items.push_back({whole[size_t(i)].cost - half, uint16_t(0x8000 | (2 * i + 1))});
+      } else {
+        items.push_back(whole[size_t(i)]);
+      }
+    }
+    if (k > 0) std::stable_sort(items.begin(), items.end(), [](const Item& a, const Item& b) { return a.cost > b.cost; });
+    const int C = int(std::min<size_t>(items.size(), size_t(max_clusters)));
+    heap.clear();
+    for (int c = 0; c < C; ++c) heap.push_back({0, c});
+    if (keep) lists.assign(size_t(C), {});
+    int32_t worst = 0;
+    for (const Item& it : items) {
+      std::pop_heap(heap.begin(), heap.end(), std::greater<>());
+      auto& top = heap.back();
+      top.first += it.cost + kUnitOverheadTiles;
+      worst = std::max(worst, top.first);
+      if (keep) lists[size_t(top.second)].push_back(it.code);
+      std::push_heap(heap.begin(), heap.end(), std::greater<>());
+    }
+    return worst + (k > 0 ? 2 : 0);
+  };
+  int best = 0;
+  int32_t least = assign(0, false);
+  for (int q = 1; q <= 4; ++q) {
+    const int k = most * q / 4;
+    if (k == 0) continue;
+    const int32_t work = assign(k, false);
+    if (work < least) {
+      least = work;
+      best = k;
+    }
+  }
+  assign(best, true);
+  for (int i = 0; i < best; ++i) p.split_unit[i] = whole[size_t(i)].code;
+  int at = 0;
+  for (size_t c = 0; c < lists.size(); ++c) {
+    p.sched_off[c] = uint16_t(at);
+    for (uint16_t code : lists[c]) p.sched[at++] = code;
+  }
+  p.sched_off[lists.size()] = uint16_t(at);
+  p.use_sched = 1;
+  return best;
+}
+
 static int tail_split_units(int64_t units, int clusters) {
   if (clusters < 2 || units <= clusters) return 0;
   const int64_t rest = units % clusters;
@@ -1404,7 +1617,10 @@ static rkv_status validate_seq(const rkv_attn_seq& s, int i, int32_t H, int32_t 
 // number and size its work units; returns the number of units.  Fills p.F,
 // p.n_seqs, p.H and p.n_whole (= all units, before any tail split).
 static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
-                          int64_t F, Params& p, int* order) {
+                          int32_t H_kv, int64_t F, Params& p, int* order) {
+  p.group = H / H_kv;
+  p.pack = !windows ? 1 : (p.group % 4 == 0 ? 4 : (p.group % 2 == 0 ? 2 : 1));
+  const int32_t unit_rows = kUnitRows / p.pack;
   for (int i = 0; i < n_seqs; ++i) order[i] = i;
   for (int i = 1; i < n_seqs; ++i)
     for (int j = i; j > 0 && seqs[order[j]].Lk > seqs[order[j - 1]].Lk; --j) std::swap(order[j], order[j - 1]);
@@ -1418,12 +1634,15 @@ static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windo
     d.Lq = s.Lq; d.Lk = s.Lk; d.q_t0 = s.q_t0; d.k_t0 = s.k_t0;
     d.q_frame_offset = s.q_frame_offset; d.block_frames = s.block_frames; d.flags = s.flags;
     if (windows) {
-      d.window_blocks = windows[order[oi]].window_blocks;
-      d.sink_blocks = windows[order[oi]].sink_blocks;
+      const rkv_attn_window& w = windows[order[oi]];
+      d.window_blocks = w.window_blocks;
+      d.block_tokens = int64_t(s.block_frames) * F;
+      d.sink_keys = int32_t(w.sink_blocks < s.Lk ? std::min<int64_t>(s.Lk, w.sink_blocks * d.block_tokens) : s.Lk);
+      d.div_block = make_fastdiv(uint32_t(s.block_frames));
     }
-    d.n_qblocks = (s.Lq + kUnitRows - 1) / kUnitRows;   // 512-row blocks, one per CTA pair
+    d.n_qblocks = (s.Lq + unit_rows - 1) / unit_rows;   // blocks of rows, one per CTA pair
     d.unit_begin = int32_t(units);
-    units += int64_t(d.n_qblocks) * H;
+    units += int64_t(d.n_qblocks) * (H / p.pack);
   }
   p.F = uint32_t(F);
   p.n_seqs = n_seqs;
@@ -1434,8 +1653,11 @@ static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windo
 }
 
 // The masks of a windowed launch.
-static rkv_status validate_windows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs) {
+static rkv_status validate_windows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs,
+                                   int64_t F) {
   for (int i = 0; i < n_seqs; ++i) {
+    if (int64_t(seqs[i].q_frame_offset) + (seqs[i].Lq - 1) / F >= (int64_t(1) << 31) - 1)
+      return fail(RKV_ERR_UNSUPPORTED, "seq %d: a query row's frame is 2^31 or more", i);
     if (seqs[i].block_frames < 1) return fail(RKV_ERR_INVALID_ARG, "seq %d: block_frames must be >= 1 with a window", i);
     if (windows[i].window_blocks < 0 || windows[i].sink_blocks < 0)
       return fail(RKV_ERR_INVALID_ARG, "seq %d: window_blocks and sink_blocks must be >= 0", i);
@@ -1463,7 +1685,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
     st = validate_seq(seqs[i], i, H, H_kv);
     if (st != RKV_OK) return st;
   }
-  if (windows && (st = validate_windows(seqs, windows, n_seqs)) != RKV_OK) return st;
+  if (windows && (st = validate_windows(seqs, windows, n_seqs, int64_t(rope->grid_h) * rope->grid_w)) != RKV_OK) return st;
   // outputs may not share a byte with any input or other output; row-strided
   // views of one tensor with disjoint heads (a launch over head slices) pass
   const int64_t row_bytes = int64_t(H) * kHD * 2, kv_bytes = int64_t(H_kv) * kHD * 2;
@@ -1483,8 +1705,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
   memset(&p, 0, sizeof(p));
   const int64_t F = int64_t(rope->grid_h) * rope->grid_w;
   int order[RKV_MAX_SEQS];
-  const int64_t units = plan_units(seqs, windows, n_seqs, H, F, p, order);
-  p.group = H / H_kv;
+  const int64_t units = plan_units(seqs, windows, n_seqs, H, H_kv, F, p, order);
 
   int64_t t_lo = INT64_MAX, t_hi = INT64_MIN;
   for (int oi = 0; oi < n_seqs; ++oi) {
@@ -1525,6 +1746,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
     entries += int64_t(p.ax_npos[a]) * p.ax_nch[a];
     first += pairs[a];
   }
+  if (no_table) entries = 0;
   if (entries > kMaxTabEntries)
     return fail(RKV_ERR_UNSUPPORTED, "RoPE positions need %lld cos/sin table entries (max %d)", (long long)entries,
                 kMaxTabEntries);
@@ -1570,30 +1792,33 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
   // Units of different cost (frame-block-masked sequences, or sequences of
   // different lengths in one launch) get a longest-first schedule; units of
   // one cost keep round-robin with the tail split below.
-  const bool sched = build_schedule(p, units, max_clusters);
-  // tail split: the last n_split units run as two half-units each when the
-  // workspace can hold their partial results and every such unit has >= 2
-  // key tiles
-  int n_split = sched ? 0 : tail_split_units(units, max_clusters);
-  if (workspace_bytes < kWorkspaceBytes + size_t(2 * n_split) * kPartBytesPerItem) n_split = 0;
+  // (attn_fwd_window: a schedule of its own.)
+  int n_split = 0;
+  if (windows) {
+    const size_t room = workspace_bytes > kWorkspaceBytes ? (workspace_bytes - kWorkspaceBytes) / (2 * kPartBytesPerItem) : 0;
+    n_split = build_window_schedule(p, units, max_clusters, int(std::min<size_t>(room, kMaxSplit)));
+  } else {
+    // tail split: the last n_split units run as two half-units each when the
+    // workspace can hold their partial results and every such unit has >= 2
+    // key tiles
+    const bool sched = build_schedule(p, units, max_clusters);
+    n_split = sched ? 0 : tail_split_units(units, max_clusters);
+    if (workspace_bytes < kWorkspaceBytes + size_t(2 * n_split) * kPartBytesPerItem) n_split = 0;
+  }
   CombineArgs ca;
   memset(&ca, 0, sizeof(ca));
   for (int k = 0; k < n_split; ++k) {
-    const int64_t u = units - n_split + k;
-    int si = 0;
-    while (si + 1 < n_seqs && u >= p.seq[si + 1].unit_begin) ++si;
-    const SeqDev& d = p.seq[si];
-    const int64_t local = u - d.unit_begin;
-    const int head = int(local / d.n_qblocks);
-    const int ord = int(local - int64_t(head) * d.n_qblocks);
-    const int qb = d.block_frames > 0 ? (d.n_qblocks - 1 - ord) : ord;
-    if (host_unit(p, int(u)).nkt < 2) { n_split = 0; break; }
+    const int64_t u = windows ? int64_t(p.split_unit[k]) : units - n_split + k;
+    const Unit un = host_unit(p, int(u));
+    if (!windows && un.nkt < 2) { n_split = 0; break; }
+    const SeqDev& d = p.seq[un.si];
     ca.unit[k].o = d.o;
     ca.unit[k].o_stride_bytes = d.o_stride_bytes;
     ca.unit[k].Lq = d.Lq;
-    ca.unit[k].head = head;
-    ca.unit[k].row0 = qb * kUnitRows;
+    ca.unit[k].head = un.head;
+    ca.unit[k].row0 = windows ? un.row0 : un.qb * kUnitRows;
   }
+  ca.pack = p.pack;
   ca.n_split = n_split;
   p.n_whole = int32_t(units - n_split);
   p.n_split = n_split;
@@ -1659,11 +1884,12 @@ extern "C" rkv_status attn_fwd_varlen_debug(const rkv_attn_seq* seqs, int32_t n_
 // The mask and unit plan on the host, for rkv_attn_mask_rows (windows and the
 // sink / begin arrays null) and rkv_attn_window_rows.
 static rkv_status host_mask(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs, int32_t H,
-                            const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
+                            int32_t H_kv, const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin, int64_t* row_limit,
                             int32_t* unit_tiles, int64_t* n_units) {
   if (!seqs || n_seqs < 1) return fail(RKV_ERR_INVALID_ARG, "need at least one sequence");
   if (n_seqs > RKV_MAX_SEQS) return fail(RKV_ERR_UNSUPPORTED, "at most %d sequences per launch", RKV_MAX_SEQS);
   if (H < 1) return fail(RKV_ERR_INVALID_ARG, "H must be >= 1");
+  if (H_kv < 1 || H % H_kv) return fail(RKV_ERR_INVALID_ARG, "H %d must be a multiple of H_kv %d", H, H_kv);
   rkv_status st = check_rope(rope, kHD);
   if (st != RKV_OK) return st;
   if (!row_limit) return fail(RKV_ERR_INVALID_ARG, "row_limit is NULL");
@@ -1674,21 +1900,24 @@ static rkv_status host_mask(const rkv_attn_seq* seqs, const rkv_attn_window* win
     if (s.block_frames > 0 && s.q_frame_offset < 0)
       return fail(RKV_ERR_INVALID_ARG, "seq %d: q_frame_offset must be >= 0 with a mask", i);
   }
-  if (windows && (st = validate_windows(seqs, windows, n_seqs)) != RKV_OK) return st;
+  if (windows && (st = validate_windows(seqs, windows, n_seqs, int64_t(rope->grid_h) * rope->grid_w)) != RKV_OK) return st;
   Params p;
   memset(&p, 0, sizeof(p));
   int order[RKV_MAX_SEQS], where[RKV_MAX_SEQS];
-  const int64_t units = plan_units(seqs, windows, n_seqs, H, int64_t(rope->grid_h) * rope->grid_w, p, order);
+  const int64_t units = plan_units(seqs, windows, n_seqs, H, H_kv, int64_t(rope->grid_h) * rope->grid_w, p, order);
   if (units >= (int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   for (int oi = 0; oi < n_seqs; ++oi) where[order[oi]] = oi;
   int64_t off = 0;
   for (int i = 0; i < n_seqs; ++i) {
     const SeqDev& d = p.seq[where[i]];
     for (int r = 0; r < d.Lq; ++r) {
-      row_limit[off + r] = row_kv_limit(d, p, r);
       if (windows) {
-        row_sink[off + r] = row_kv_sink(d, p, r);
-        row_begin[off + r] = row_kv_begin(d, p, r);
+        const RowView v = row_view(d, p, r);
+        row_limit[off + r] = v.limit;
+        row_sink[off + r] = v.sink;
+        row_begin[off + r] = v.lo;
+      } else {
+        row_limit[off + r] = row_kv_limit(d, p, r);
       }
     }
     off += d.Lq;
@@ -1698,7 +1927,7 @@ static rkv_status host_mask(const rkv_attn_seq* seqs, const rkv_attn_window* win
       const Unit un = host_unit(p, int(u));
       unit_tiles[4 * u + 0] = order[un.si];
       unit_tiles[4 * u + 1] = un.head;
-      unit_tiles[4 * u + 2] = un.qb;
+      unit_tiles[4 * u + 2] = windows ? un.row0 : un.qb;
       unit_tiles[4 * u + 3] = un.nkt;
     }
   }
@@ -1711,17 +1940,17 @@ extern "C" rkv_status rkv_attn_mask_rows(const rkv_attn_seq* seqs, int32_t n_seq
                                          int64_t* n_units) {
   NvtxRange nvtx_range("rkv_attn_mask_rows");
   clear_error();
-  return host_mask(seqs, nullptr, n_seqs, H, rope, nullptr, nullptr, row_limit, unit_tiles, n_units);
+  return host_mask(seqs, nullptr, n_seqs, H, H, rope, nullptr, nullptr, row_limit, unit_tiles, n_units);
 }
 
 extern "C" rkv_status rkv_attn_window_rows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs,
-                                           int32_t H, const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin,
+                                           int32_t H, int32_t H_kv, const rkv_rope3d* rope, int64_t* row_sink, int64_t* row_begin,
                                            int64_t* row_limit, int32_t* unit_tiles, int64_t* n_units) {
   NvtxRange nvtx_range("rkv_attn_window_rows");
   clear_error();
   if (!windows) return fail(RKV_ERR_INVALID_ARG, "windows is NULL");
   if (!row_sink || !row_begin) return fail(RKV_ERR_INVALID_ARG, "row_sink/row_begin is NULL");
-  return host_mask(seqs, windows, n_seqs, H, rope, row_sink, row_begin, row_limit, unit_tiles, n_units);
+  return host_mask(seqs, windows, n_seqs, H, H_kv, rope, row_sink, row_begin, row_limit, unit_tiles, n_units);
 }
 
 extern "C" rkv_status rkv_attn_status(void* workspace, void* stream) {

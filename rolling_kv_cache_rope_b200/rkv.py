@@ -124,7 +124,7 @@ _lib.attn_fwd_window.argtypes = [_c.POINTER(rkv_attn_seq), _c.POINTER(rkv_attn_w
                                  _c.c_void_p]
 _lib.rkv_attn_window_rows.restype = _c.c_int
 _lib.rkv_attn_window_rows.argtypes = [_c.POINTER(rkv_attn_seq), _c.POINTER(rkv_attn_window), _c.c_int32, _c.c_int32,
-                                      _c.POINTER(rkv_rope3d), _c.POINTER(_c.c_int64), _c.POINTER(_c.c_int64),
+                                      _c.c_int32, _c.POINTER(rkv_rope3d), _c.POINTER(_c.c_int64), _c.POINTER(_c.c_int64),
                                       _c.POINTER(_c.c_int64), _c.POINTER(_c.c_int32), _c.POINTER(_c.c_int64)]
 _lib.kvcache_paged_insert.restype = _c.c_int
 _lib.kvcache_paged_insert.argtypes = [_c.POINTER(rkv_paged_cache), _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int32,
@@ -512,12 +512,13 @@ def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, str
     return workspace
 
 
-def attn_window_rows(seqs, windows, H, rope):
+def attn_window_rows(seqs, windows, H, rope, H_kv=None):
     """The mask and key-tile plan attn_fwd_window uses, evaluated on the host
     by the kernel's own code (no GPU needed).  ``seqs``: dicts with Lq, Lk,
     block_frames and optional q_frame_offset.  Returns (sink, begin, limit,
     units): lists per sequence of per-row key ranges [0, sink) and [begin,
-    limit), and units as attn_mask_rows gives them."""
+    limit), and int32 [n_units, 4] rows of (sequence, first head, first query
+    row, 128-key tiles processed)."""
     import numpy as np
     arr = (rkv_attn_seq * len(seqs))(*[
         rkv_attn_seq(Lq=int(s["Lq"]), Lk=int(s["Lk"]), q_frame_offset=int(s.get("q_frame_offset", 0)),
@@ -528,7 +529,7 @@ def attn_window_rows(seqs, windows, H, rope):
     units = np.zeros((max(1, sum(int(H) * ((x + 511) // 512) for x in lq)), 4), dtype=np.int32)
     n = ctypes.c_int64(0)
     p64 = ctypes.POINTER(ctypes.c_int64)
-    _check(_lib.rkv_attn_window_rows(arr, win, len(seqs), int(H), ctypes.byref(rope),
+    _check(_lib.rkv_attn_window_rows(arr, win, len(seqs), int(H), int(H if H_kv is None else H_kv), ctypes.byref(rope),
                                      *[g.ctypes.data_as(p64) for g in got],
                                      units.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), ctypes.byref(n)))
     at = np.cumsum([0] + lq)

@@ -115,6 +115,32 @@ def test_grouped_heads(H, G):
     run([spec(300, 420, 120, 150, 10)], H, G, (1, 1))
 
 
+@pytest.mark.parametrize("H,G", [(2, 1), (3, 2), (2, 4), (1, 8)])
+def test_split_units(H, G):
+    # few units of many key tiles run as halves, merged into the output
+    run([spec(900, 2500, 1600, 1300, 140)], H, G, (1, 1))
+
+
+def test_windows_with_rope_and_grouped_heads():
+    run([spec(500, 720, 10, 3, 1, 1, (True, True))], 2, 4, (4, 6))
+    run([spec(500, 720, 10, 3, 1, 1, (True, True))], 2, 2, (4, 6))
+
+
+def test_small_workspace():
+    # with room for the status word only nothing is split: the same result within rounding
+    need_gpu()
+    from rolling_kv_cache_rope_b200 import rkv
+    q, k, v = (to_dev(bf16_normal_bits(30 + i, (n, 2, D))) for i, n in enumerate((700, 2000, 2000)))
+    outs = []
+    for ws in (None, torch.empty(256, dtype=torch.uint8, device="cuda")):
+        o = torch.full_like(q, float("nan"))
+        s = rkv.AttnSeq(q, k, v, o, rope_q=False, rope_k=False, block_frames=1, q_frame_offset=1300)
+        rkv.rkv_attn_status(rkv.attn_fwd_window([s], [(1000, 3)], rkv.make_rope(1, 1), workspace=ws))
+        outs.append(to_f64(o))
+    # both round P and the output to bf16: half a step each of the weights' and of the output's size
+    assert np.abs(outs[0] - outs[1]).max() <= 4 * 2.0 ** -8 * np.abs(outs[0]).max()
+
+
 @pytest.mark.parametrize("rope", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("Lq,Lk,off,window,sinks,block", [
     (72, 120, 2, 2, 1, 1), (100, 121, 1, 1, 1, 3), (600, 960, 15, 6, 2, 1), (600, 960, 15, 2, 1, 3)])
@@ -143,7 +169,8 @@ def test_equal_units_with_tail_split():
 
 
 def test_no_window_is_the_block_mask():
-    # bit-identical to attn_fwd_varlen where the mask and the heads are the same
+    # bit-identical to attn_fwd_varlen where the mask and the heads are the same (and the workspace
+    # leaves no room to split units, which joins two halves' sums in another order)
     need_gpu()
     from rolling_kv_cache_rope_b200 import rkv
     q, k, v = (to_dev(bf16_normal_bits(20 + i, (n, 2, D))) for i, n in enumerate((480, 720, 720)))
@@ -152,7 +179,11 @@ def test_no_window_is_the_block_mask():
     for window in (None, 0, 1000):
         o = torch.full_like(q, float("nan"))
         s = rkv.AttnSeq(q, k, v, o, q_t0=10, k_t0=0, block_frames=3, q_frame_offset=10)
-        ws = rkv.attn_fwd_varlen([s], rope) if window is None else rkv.attn_fwd_window([s], [(window, 0)], rope)
+        ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+        if window is None:
+            rkv.attn_fwd_varlen([s], rope, workspace=ws)
+        else:
+            rkv.attn_fwd_window([s], [(window, 0)], rope, workspace=ws)
         rkv.rkv_attn_status(ws)
         outs.append(o)
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])

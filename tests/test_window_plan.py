@@ -15,10 +15,14 @@ def rkv(lib_path):
     return m
 
 
-def check(rkv, grid, seqs, windows, H=2):
+def check(rkv, grid, seqs, windows, H=2, H_kv=2):
     F = grid[0] * grid[1]
-    sink, begin, limit, units = rkv.attn_window_rows(seqs, windows, H, rkv.make_rope(*grid))
-    at = 0
+    sink, begin, limit, units = rkv.attn_window_rows(seqs, windows, H, rkv.make_rope(*grid), H_kv)
+    G = H // H_kv
+    pack = 4 if G % 4 == 0 else 2 if G % 2 == 0 else 1
+    rows = 512 // pack
+    want_units = sorted((i, h, r) for i, s in enumerate(seqs) for h in range(0, H, pack) for r in range(0, s["Lq"], rows))
+    assert sorted(map(tuple, units[:, :3].tolist())) == want_units
     for i, (s, (w, k)) in enumerate(zip(seqs, windows)):
         Lq, Lk = s["Lq"], s["Lk"]
         seen = frame_window_visible(Lq, Lk, F, s.get("q_frame_offset", 0), s["block_frames"], w, k)
@@ -27,19 +31,17 @@ def check(rkv, grid, seqs, windows, H=2):
         assert np.array_equal(got, seen), (s, w, k)
         # a unit's tiles: every tile that holds a key one of its rows sees, or one tile; a tile between
         # the sinks and the window may be taken in where the two runs meet
-        for si, head, qb, tiles in units:
+        for si, head, row0, tiles in units:
             if si != i:
                 continue
-            rows = seen[qb * 512:(qb + 1) * 512].any(0)
+            last = min(Lq, row0 + rows) - 1
             pad = np.zeros(-(-Lk // 128) * 128, dtype=bool)
-            pad[:Lk] = rows
+            pad[:Lk] = seen[row0:last + 1].any(0)
             need = pad.reshape(-1, 128).any(1)
-            assert need.sum() <= tiles, (s, w, k, qb, tiles)
+            assert need.sum() <= tiles, (s, w, k, row0, tiles)
             # never more than the span of the rows' windows and the sinks
-            first, last = limit[i][qb * 512] * 0 + begin[i][qb * 512], limit[i][min(Lq, (qb + 1) * 512) - 1]
-            most = -(-int(last) // 128) - int(first) // 128 + -(-int(sink[i].max()) // 128)
-            assert tiles <= max(1, most), (s, w, k, qb, tiles, most)
-        at += Lq
+            most = -(-int(limit[i][last]) // 128) - int(begin[i][row0]) // 128 + -(-int(sink[i].max()) // 128)
+            assert tiles <= max(1, most), (s, w, k, row0, tiles, most)
 
 
 @pytest.mark.parametrize("grid,Lq,Lk,off,block,window,sinks", [
@@ -55,7 +57,8 @@ def check(rkv, grid, seqs, windows, H=2):
     ((30, 52), 1560, 32760, 20, 3, 0, 5),
 ])
 def test_plan_matches_oracle(rkv, grid, Lq, Lk, off, block, window, sinks):
-    check(rkv, grid, [dict(Lq=Lq, Lk=Lk, q_frame_offset=off, block_frames=block)], [(window, sinks)])
+    for H, H_kv in ((2, 2), (4, 1), (6, 1), (6, 3)):
+        check(rkv, grid, [dict(Lq=Lq, Lk=Lk, q_frame_offset=off, block_frames=block)], [(window, sinks)], H, H_kv)
 
 
 def test_plan_random(rkv):
@@ -67,7 +70,8 @@ def test_plan_random(rkv):
             seqs.append(dict(Lq=int(rng.integers(1, 1300)), Lk=int(rng.integers(1, 2000)),
                              q_frame_offset=int(rng.integers(0, 100)), block_frames=int(rng.integers(1, 4))))
             windows.append((int(rng.integers(0, 30)), int(rng.integers(0, 8))))
-        check(rkv, grid, seqs, windows, H=1)
+        G = int(rng.integers(1, 9))
+        check(rkv, grid, seqs, windows, H=G, H_kv=1)
 
 
 def desc(rkv, **kw):
@@ -100,6 +104,13 @@ def test_window_rejects(rkv, seq, win, call, frag):
                                    ctypes.byref(rope), ctypes.c_void_p(a["ws"]), 256, None)
     assert st == rkv.RKV_ERR_INVALID_ARG, rkv.rkv_last_error_string()
     assert frag in rkv.rkv_last_error_string()
+
+
+def test_window_rejects_far_frames(rkv):
+    s, w, rope = desc(rkv, q_frame_offset=2 ** 31 - 1), rkv.rkv_attn_window(1, 0), rkv.make_rope(1, 1)
+    st = rkv.lib().attn_fwd_window(ctypes.byref(s), ctypes.byref(w), 1, 4, 2, 128, 0.1, ctypes.byref(rope),
+                                   ctypes.c_void_p(0x40000000), 256, None)
+    assert st == rkv.RKV_ERR_UNSUPPORTED and "frame" in rkv.rkv_last_error_string()
 
 
 def test_window_rows_rejects(rkv):
