@@ -317,8 +317,9 @@ struct Unit {
   int si, head, qb, nkt;
   int kt0, kt1;   // key tiles [kt0, kt1) of this work item
   int part;       // -1: whole unit; else index of the item's partial-result slot
-  // windowed launches list the key tiles of the sinks and of the window: entry
-  // j of the list is tile j below `ns` and tile j + skip from there on
+  // windowed launches list the key tiles of the sinks, then those of the window
+  // (the other order measured the same or 3% slower): entry j of the list is
+  // tile j below `ns` and tile j + skip from there on
   int ns, skip;
   int32_t lo, sink, hi;   // keys some row of the unit sees: [0, sink) and [lo, hi)
   int32_t row0;           // first query row (of each of the unit's heads)
@@ -699,29 +700,33 @@ __device__ __forceinline__ void warp_view_tile(uint32_t at, int kbase, bool& mas
 // Bits [0, n) of a word, n brought into [0, 32].
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// The tile whose first key is kbase, of which one thread's row sees the keys in
-// [0, sink) and [lo, limit) (its bounds at `row` in shared memory): its scores
-// are read from TMEM 32 at a time, twice, so that the path needs few registers
-// beside the row that the unmasked path holds.  A warp's 32 rows cut through
-// one or two of the four chunks; the others take no select.
-__device__ __forceinline__ void window_chunk(uint32_t (&r)[32], uint32_t tS, uint32_t row, int kbase, int ch) {
-  ptx::tmem_ld32(tS + ch * 32, r);
+// The softmax of a tile (first key kbase) of which one thread's row sees the
+// keys in [0, sink) and [lo, limit) (its bounds at `row` in shared memory): P
+// written over S as in exp_store_tile; returns the running max with this
+// tile's, and the sum of the P.  m: the running max so far; P is taken against
+// the new one where it moves.  Out of line, in loops over 32 scores at a time
+// read from TMEM twice: the hot loop's code and registers stay as they are
+// without it (inlined, the instruction cache missed 2.7 times as often and
+// the denoise pass took 20% longer).  A warp's 32 rows cut through one or two of
+// the four chunks; the others take no select.
+__device__ __noinline__ float2 window_tile(uint32_t tS, uint32_t row, int kbase, float scale_log2, float m) {
   const uint4 x = ptx::lds128(row);
-  const int at = kbase + 32 * ch;
-  const uint32_t seen = low_bits(int(x.x) - at) & (~low_bits(int(x.y) - at) | low_bits(int(x.z) - at));
-  ptx::tmem_wait_ld();
-  if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
+  auto chunk = [&](uint32_t (&r)[32], int ch) {
+    ptx::tmem_ld32(tS + ch * 32, r);
+    const int at = kbase + 32 * ch;
+    const uint32_t seen = low_bits(int(x.x) - at) & (~low_bits(int(x.y) - at) | low_bits(int(x.z) - at));
+    ptx::tmem_wait_ld();
+    if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!(seen & (1u << i))) r[i] = 0xFF800000u;   // -inf
-  }
-}
-__device__ __forceinline__ float window_tile_max(uint32_t tS, uint32_t row, int kbase) {
+      for (int i = 0; i < 32; ++i)
+        if (!(seen & (1u << i))) r[i] = 0xFF800000u;   // -inf
+    }
+  };
   float mx = -INFINITY;
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     uint32_t r[32];
-    window_chunk(r, tS, row, kbase, ch);
+    chunk(r, ch);
     float m2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -730,29 +735,44 @@ __device__ __forceinline__ float window_tile_max(uint32_t tS, uint32_t row, int 
     }
     mx = max3f(mx, m2[0], m2[1]);
   }
-  return mx;
-}
-// exp_store_tile of such a tile: chunk ch's P takes columns 16 ch .. of S,
-// which chunks up to ch have been read from.
-__device__ __forceinline__ float window_tile_exp(uint32_t tS, uint32_t row, int kbase, float scale_log2, float m_use) {
-  float2 acc = make_float2(0.f, 0.f);
+  const float m_new = fmaxf(m, mx * scale_log2);
+  if (m_new > m + kRescaleLog2) m = m_new;
+  const float m_use = m == -INFINITY ? 0.f : m;   // a row that has seen nothing so far may see nothing here
+  // (summed in exp_store_tile's order: the same bits)
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-  for (int ch = 0; ch < 4; ++ch) {
+  for (int ch = 0; ch < 4; ++ch) {   // P of chunk ch takes columns 16 ch .. of S, which have been read
     uint32_t r[32], pk[16];
-    window_chunk(r, tS, row, kbase, ch);
-    float2 a2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    chunk(r, ch);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+      const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
                                   make_float2(scale_log2, scale_log2), make_float2(-m_use, -m_use));
-      const float2 pp = make_float2(ptx::ex2_approx(x.x), ptx::ex2_approx(x.y));   // exp2(-inf) = 0: hidden keys
-      a2[i & 1] = __fadd2_rn(a2[i & 1], pp);
+      const float2 pp = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));   // exp2(-inf) = 0: hidden keys
+      acc[i & 3] = __fadd2_rn(acc[i & 3], pp);
       pk[i] = pack_bf16x2(pp.x, pp.y);
     }
     ptx::tmem_st16(tS + ch * 16, pk);
-    acc = __fadd2_rn(acc, __fadd2_rn(a2[0], a2[1]));
   }
-  return acc.x + acc.y;
+  const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+  return make_float2(m_new, (a01.x + a01.y) + (a23.x + a23.y));
+}
+// Weights of zero for a tile of which no row of the warp sees a key.
+__device__ __noinline__ void window_tile_hidden(uint32_t tS) {
+  const uint32_t zero[16] = {};
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) ptx::tmem_st16(tS + ch * 16, zero);
+}
+// Rows of a V tile (at `tile` in shared memory, first key `base`) that no row
+// of the unit sees have weights of zero, and zero times an infinity or a NaN
+// would enter every sum: they are overwritten with zeros (a row is 128
+// contiguous bytes, swizzled only within itself).  By a whole warp.
+__device__ __noinline__ void window_clear_v(uint32_t tile, int base, int lo, int hi, int sink) {
+  for (int x = int(threadIdx.x & 31); x < kBN * 8; x += 32) {
+    const int key = base + (x >> 3);
+    if (!(key < hi && key >= lo) && key >= sink) ptx::sts128(tile + uint32_t(x) * 16u, make_uint4(0u, 0u, 0u, 0u));
+  }
+  ptx::fence_proxy_async_smem();
 }
 
 // K-major operand (rows of 128 bf16 in two 64-column 128B-swizzled halves):
@@ -894,6 +914,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       float m = -INFINITY, l = 0.f;
       RowStats rs = {0u, 0u, 0u, 0u};
       for (int j = un.kt0; j < un.kt1; ++j, ++g) {
+        bool masked, hidden = false;
+        if constexpr (kWindow)   // read while the scores are still being computed
+          warp_view_tile(sbase + kOffViews + uint32_t(warp) * kWarpBounds, tile_at<kWindow>(un, j) * kBN, masked, hidden);
         if (!wait_warp(c, bar(c, B_SFULL + wg), g & 1u, 1)) goto done;
         ptx::tc_fence_after();
         uint32_t sr[4][32];
@@ -904,9 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int lim = kbase + kBN > my_limit ? int(my_limit - kbase) : kBN;
         // partial tile for some row of the warp: hide keys at or past each
         // row's limit (the keys of a row's mask are a prefix)
-        bool masked, hidden = false;
         if constexpr (!kWindow) masked = __any_sync(0xffffffffu, lim < kBN);
-        else warp_view_tile(sbase + kOffViews + uint32_t(warp) * kWarpBounds, int(kbase), masked, hidden);
         const float m_old = m;
         float m_new, tile_sum;
         bool need;
@@ -924,19 +945,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             tile_sum = exp_store_tile(sr, tS, scale_log2, m);
           }
         } else if (kWindow && hidden) {
-          // weights of zero, with neither maximum nor exponentials
-          const uint32_t zero[16] = {};
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) ptx::tmem_st16(tS + ch * 16, zero);
+          window_tile_hidden(tS);
           m_new = m;
           tile_sum = 0.f;
           need = false;
-        } else if (kWindow && masked) {
-          const uint32_t row = sbase + kOffRows + uint32_t(tid) * kRowBounds;
-          m_new = fmaxf(m, window_tile_max(tS, row, int(kbase)) * scale_log2);
+        } else if constexpr (kWindow) {   // partly hidden, or the item's first
+          const float2 r = window_tile(tS, sbase + kOffRows + uint32_t(tid) * kRowBounds, int(kbase), scale_log2, m);
+          m_new = r.x;
+          tile_sum = r.y;
           need = m_new > m + kRescaleLog2;
           if (need) m = m_new;
-          tile_sum = window_tile_exp(tS, row, int(kbase), scale_log2, m == -INFINITY ? 0.f : m);
         } else {
           if (masked) {
 #pragma unroll
@@ -1167,28 +1185,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       if (!ok) drain_loads(bar(c, B_VFULL), it, kStages, 0u, 0u, p.timeout_ns);
     } else if (kWindow && warp == 15) {
       // ===================== V landed, unseen rows cleared -> tell the leader =====================
-      // Rows of an edge tile that no row of the unit sees have weights of
-      // zero, and zero times an infinity or a NaN would enter every sum: they
-      // are overwritten with zeros (a row is 128 contiguous bytes, swizzled
-      // only within itself).
+      // Lane 0 waits for the tiles and reports them; the other lanes only meet
+      // it at the edge tiles, which the warp clears together.  After a wait
+      // that gave up lane 0 goes on to the next meeting, where all leave.
       uint32_t it = 0;
-      bool ok = true;
-      for (int k = 0; ok && k < n_items; ++k) {
+      bool ok = true, met = true;
+      for (int k = 0; met && k < n_items; ++k) {
         const Unit un = decode_unit<kWindow>(p, item_at<kWindow>(p, cluster, n_clusters, k));
         for (int j = un.kt0; j < un.kt1; ++j, ++it) {
           const uint32_t st = it % kStages, n = it / kStages;
-          if (!wait_warp(c, bar(c, B_VFULL + st), n & 1u, 17)) { ok = false; break; }
+          if (lane == 0 && ok) ok = wait_phase(c, bar(c, B_VFULL + st), n & 1u, 17);
           const int base = tile_at<kWindow>(un, j) * kBN;
           if (!((base + kBN <= un.hi && base >= un.lo) || base + kBN <= un.sink)) {
-            for (int x = lane; x < kBN * 8; x += 32) {
-              const int key = base + (x >> 3);
-              if (!(key < un.hi && key >= un.lo) && key >= un.sink)
-                ptx::sts128(sV + st * kVStageBytes + uint32_t(x) * 16u, make_uint4(0u, 0u, 0u, 0u));
-            }
-            ptx::fence_proxy_async_smem();
+            met = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!met) break;
+            window_clear_v(sV + st * kVStageBytes, base, un.lo, un.hi, un.sink);
+            __syncwarp();
           }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(lbar(B_VREADY + st));
+          if (lane == 0 && ok) ptx::mbar_arrive_cluster(lbar(B_VREADY + st));
         }
       }
     } else if (!kWindow && warp == 15 && lane == 0) {
@@ -1554,6 +1568,11 @@ static int build_window_schedule(Params& p, int64_t units, int max_clusters, int
   }
   assign(best, true);
   for (int i = 0; i < best; ++i) p.split_unit[i] = whole[size_t(i)].code;
+  // each pair takes its items in the order of the units, head by head, so that
+  // the pairs in flight share the K/V tiles of few heads in L2
+  auto unit_of = [&](uint16_t code) { return code & 0x8000 ? p.split_unit[(code & 0x7FFF) >> 1] : code; };
+  for (auto& list : lists)
+    std::stable_sort(list.begin(), list.end(), [&](uint16_t a, uint16_t b) { return unit_of(a) < unit_of(b); });
   int at = 0;
   for (size_t c = 0; c < lists.size(); ++c) {
     p.sched_off[c] = uint16_t(at);
