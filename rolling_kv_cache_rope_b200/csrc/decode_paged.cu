@@ -631,23 +631,45 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ptx::pdl_wait();   // the main launch's parts are written
   ptx::pdl_launch_dependents();
+  // Main block b = blockIdx.x may hold the first part of an item that goes on in
+  // the blocks after it.  A row is joined by `per` warps (all eight where there
+  // is one row), each with every per-th part; they meet in order in shared
+  // memory.  The first parts are loaded beside the record that says whether and
+  // how many there are: what is not a part is not used.
+  const int per = a.rows_blk == 1 ? 8 : (a.rows_blk == 2 ? 4 : (a.rows_blk <= 4 ? 2 : 1));
+  const int b0 = blockIdx.x, w0 = warp % per, r = int(blockIdx.y) * (8 / per) + warp / per;
+  const bool row_ok = r < a.rows_blk;
+  constexpr int kAheadParts = 4;
+  float2 ml0 = make_float2(-INFINITY, 0.f), ml1 = ml0;   // part w0 + lane * per; slot 1 of the first block
+  float4 o_ahead[kAheadParts], o1 = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row_ok) {
+    if (b0 + w0 + lane * per < a.main_blocks) ml0 = a.part_ml[part_row(a, b0, 0, w0 + lane * per, r)];
+    if (w0 == 0) {
+      ml1 = a.part_ml[part_row(a, b0, 1, 0, r)];
+      o1 = *reinterpret_cast<const float4*>(a.part_o + part_row(a, b0, 1, 0, r) * kHD + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kAheadParts; ++i)
+      if (b0 + w0 + i * per < a.main_blocks)
+        o_ahead[i] = *reinterpret_cast<const float4*>(a.part_o + part_row(a, b0, 0, w0 + i * per, r) * kHD + 4 * lane);
+  }
   const BlockRec rec = a.recs[blockIdx.x];
 
   if (rec.parts > 0) {
-    // Main block b = blockIdx.x holds the item's first part.  A row is joined
-    // by `per` warps (all eight where there is one row), each with every
-    // per-th part; they meet in order in shared memory.
-    const int per = a.rows_blk == 1 ? 8 : (a.rows_blk == 2 ? 4 : (a.rows_blk <= 4 ? 2 : 1));
-    const int b0 = blockIdx.x, n = rec.parts;
+    const int n = rec.parts;
     const int rows_here = min(a.rows - rec.join_blk * a.rows_tile, a.rows_tile);
-    const int r = int(blockIdx.y) * (8 / per) + warp / per, w0 = warp % per;
     float M = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < rows_here) {
+      if (w0 == 0 && rec.slot == 1) {
+        if (lane == 0) ml0 = ml1;
+        o_ahead[0] = o1;
+      }
       for (int i0 = w0; i0 < n; i0 += 32 * per) {   // 32 parts at a time, one a lane
         const int mine = i0 + lane * per;
-        float2 x = make_float2(-INFINITY, 0.f);
-        if (mine < n) x = a.part_ml[part_row(a, b0, rec.slot, mine, r)];
+        float2 x = ml0;
+        if (i0 != w0 && mine < n) x = a.part_ml[part_row(a, b0, rec.slot, mine, r)];
+        if (mine >= n) x = make_float2(-INFINITY, 0.f);
         float nm = x.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
@@ -661,16 +683,23 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
         sum = sum * old + add;
         acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
         const int count = min(32, (n - i0 + per - 1) / per);
-#pragma unroll 8
-        for (int i = 0; i < count; ++i) {
+        auto take = [&](int i, float4 y) {
           const float g = __shfl_sync(0xffffffffu, f, i);
-          const float4 y = *reinterpret_cast<const float4*>(
-              a.part_o + part_row(a, b0, rec.slot, i0 + i * per, r) * kHD + 4 * lane);
           acc.x += y.x * g;
           acc.y += y.y * g;
           acc.z += y.z * g;
           acc.w += y.w * g;
+        };
+        int i1 = 0;
+        if (i0 == w0) {
+#pragma unroll
+          for (int i = 0; i < kAheadParts; ++i)
+            if (i < count) take(i, o_ahead[i]);
+          i1 = min(count, kAheadParts);
         }
+#pragma unroll 4
+        for (int i = i1; i < count; ++i)
+          take(i, *reinterpret_cast<const float4*>(a.part_o + part_row(a, b0, rec.slot, i0 + i * per, r) * kHD + 4 * lane));
       }
     }
     if (per > 1) {
@@ -739,6 +768,21 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       const int x = cu.c * a.step_keys + 2 * lane;
       const bool live = 2 * lane < a.step_keys;
       float2 sum = make_float2(0.f, 0.f);
+      // what is added to, and the first rows' scores, are under way before the
+      // rows' maxima are known
+      const int64_t at0 = out + token_of(cu.sp, x), at1 = out + token_of(cu.sp, x + 1);
+      const bool on0 = live && x < cu.sp.span, on1 = live && x + 1 < cu.sp.span;
+      float2 old = make_float2(0.f, 0.f);
+      if (a.weight_in && on0) old.x = a.weight_in[at0];
+      if (a.weight_in && on1) old.y = a.weight_in[at1];
+      constexpr int kAhead = 4;
+      float2 ahead[kAhead];
+      const int rows_first = min(min(a.rows, a.rows_tile), kAhead);
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r)
+        if (live && r < rows_first)
+          ahead[r] = *reinterpret_cast<const float2*>(a.scores + ((int64_t(rec.first) + t) * a.rows_blk + r) * a.step_keys +
+                                                      2 * lane);
       for (int blk = 0; blk < a.n_blk; ++blk) {
         const int x0 = rec.first + t - cu.c + blk * cu.nc;   // the item's first step in the whole list
         const int rows_here = min(a.rows - blk * a.rows_tile, a.rows_tile);
@@ -759,11 +803,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
                 ls = y.y;
               } else {
 #pragma unroll 4
-                for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_ml[part_row(a, b0, slot, i, r)].x);
-#pragma unroll 4
                 for (int i = 0; i < n; ++i) {
                   const float2 y = a.part_ml[part_row(a, b0, slot, i, r)];
-                  ls += y.x == -INFINITY ? 0.f : y.y * ptx::ex2_approx(y.x - M);
+                  const float nm = fmaxf(M, y.x);
+                  if (nm != -INFINITY) ls = ls * ptx::ex2_approx(M - nm) + y.y * ptx::ex2_approx(y.x - nm);
+                  M = nm;
                 }
               }
               if (ls > 0.f) mr = make_float2(M, 1.f / ls);
@@ -771,8 +815,20 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
           }
           const float* sc = a.scores + ((int64_t(x0) + cu.c) * a.rows_blk + r0) * a.step_keys + 2 * lane;
           const int rows = min(rows_here - r0, 32);
+          int r1 = 0;
+          if (blk == 0 && r0 == 0) {
+            r1 = rows_first;
+#pragma unroll
+            for (int r = 0; r < kAhead; ++r) {
+              const float M = __shfl_sync(0xffffffffu, mr.x, r), inv = __shfl_sync(0xffffffffu, mr.y, r);
+              if (live && r < rows_first) {
+                sum.x += ptx::ex2_approx(ahead[r].x - M) * inv;
+                sum.y += ptx::ex2_approx(ahead[r].y - M) * inv;
+              }
+            }
+          }
 #pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
+          for (int r = r1; r < rows; ++r) {
             const float M = __shfl_sync(0xffffffffu, mr.x, r), inv = __shfl_sync(0xffffffffu, mr.y, r);
             if (live) {
               const float2 y = *reinterpret_cast<const float2*>(sc + int64_t(r) * a.step_keys);
@@ -782,14 +838,8 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
           }
         }
       }
-      auto store = [&](int xx, float add) {
-        if (live && xx < cu.sp.span) {
-          const int64_t at = out + token_of(cu.sp, xx);
-          a.weight_out[at] = (a.weight_in ? a.weight_in[at] : 0.f) + add;
-        }
-      };
-      store(x, sum.x);
-      store(x + 1, sum.y);
+      if (on0) a.weight_out[at0] = old.x + sum.x;
+      if (on1) a.weight_out[at1] = old.y + sum.y;
       if (cu.sp.lo > cu.sp.se && a.weight_in != a.weight_out) {
         const int64_t gap = cu.sp.lo - cu.sp.se;
         const int64_t from = cu.sp.se + gap * cu.c / cu.nc, to = cu.sp.se + gap * (cu.c + 1) / cu.nc;
