@@ -56,6 +56,7 @@
 #include <algorithm>
 #include <functional>
 #include <mutex>
+#include <new>
 #include <queue>
 #include <utility>
 #include <vector>
@@ -1744,7 +1745,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
       t_hi = std::max<int64_t>(t_hi, int64_t(s.k_t0) + (s.Lk - 1) / F);
     }
   }
-  if (units >= (int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
+  if (units >= (windows ? int64_t(kHalfItem) : int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   if (t_lo == INT64_MAX) { t_lo = 0; t_hi = -1; }
   const int64_t n_t = t_hi - t_lo + 1;
   const int32_t pairs[3] = {rope->pairs_t, rope->pairs_h, rope->pairs_w};
@@ -1815,7 +1816,12 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
   int n_split = 0;
   if (windows) {
     const size_t room = workspace_bytes > kWorkspaceBytes ? (workspace_bytes - kWorkspaceBytes) / (2 * kPartBytesPerItem) : 0;
-    n_split = build_window_schedule(p, units, max_clusters, int(std::min<size_t>(room, kMaxSplit)));
+    try {
+      n_split = build_window_schedule(p, units, max_clusters, int(std::min<size_t>(room, kMaxSplit)));
+    } catch (const std::bad_alloc&) {   // round-robin needs no lists
+      p.use_sched = 0;
+      n_split = 0;
+    }
   } else {
     // tail split: the last n_split units run as two half-units each when the
     // workspace can hold their partial results and every such unit has >= 2

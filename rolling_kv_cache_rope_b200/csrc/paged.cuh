@@ -100,6 +100,7 @@ inline cudaError_t launch_overlapped(void (*kern)(Args), dim3 grid, int threads,
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int64_t capacity(const rkv_paged_cache* c) { return int64_t(c->max_pages) * c->page_tokens; }
 
 }  // namespace paged

@@ -96,7 +96,9 @@ def test_interleaved_pools_are_no_overlap(rkv):
     (dict(stride=128), "stride"), (dict(stride=260), "aligned"), (dict(stride=1 << 41), "stride"),
     (dict(k=0x100000000), "overlap"), (dict(v=0x200000000 + 64), "overlap"),
     (dict(weight=0x100000000), "overlap"), (dict(nxt=0x700000000, pos=0x200000000), "overlap"),
-    (dict(nxt=0x700000000, pos=0x710000000, weight=0x710000004), "overlap"),
+    (dict(nxt=0x700000000, pos=0x710000000, weight=0x710000004), "overlap"), (dict(lens=0x500000002), "4-byte"),
+    (dict(nxt=0x700000000, pos=0x710000001), "4-byte"), (dict(weight=0x500000000), "overlap"),
+    (dict(nxt=0x700000000, pos=0x700000000), "overlap"), (dict(weight=0x410000000), "overlap"),
 ])
 def test_insert_rejects(rkv, change, frag):
     assert insert(rkv, cache(rkv), **change) == rkv.RKV_ERR_INVALID_ARG
@@ -114,7 +116,8 @@ def test_insert_of_nothing_is_a_host_noop(rkv):
     (dict(scale=float("inf")), "scale"), (dict(window=-1), "window"), (dict(sinks=-1), "sinks"),
     (dict(win=0x700000000), "weight_out"), (dict(o=0x400000000), "overlap"), (dict(o=0x100000000), "overlap"),
     (dict(win=0x700000000, wout=0x700000010), "part"), (dict(wout=0x410000000), "overlap"),
-    (dict(wout=0x200000000), "overlap"), (dict(ws=0), "workspace"), (dict(ws=0x600000008), "workspace"),
+    (dict(wout=0x200000000), "overlap"), (dict(lens=0x500000001), "4-byte"), (dict(wout=0x700000002), "4-byte"),
+    (dict(lens=0x410000000), "overlap"), (dict(wout=0x500000000), "overlap"), (dict(ws=0), "workspace"), (dict(ws=0x600000008), "workspace"),
     (dict(wsb=16), "workspace"),
 ])
 def test_decode_rejects(rkv, change, frag):
@@ -133,7 +136,8 @@ def test_decode_too_many_rows(rkv):
     (dict(sinks=-1), "sinks"), (dict(recent=-1), "recent"), (dict(wout=0x710000000), "both or neither"),
     (dict(wout=0x510000010, pout=0x720000000), "overlap"), (dict(wout=0x710000000, pout=0x710000010), "overlap"),
     (dict(wout=0x100000000, pout=0x720000000), "pool"), (dict(lens_out=0x500000004), "seq_lens_out"),
-    (dict(lens_out=0x530000000), "seq_lens_out"), (dict(lens_out=0x510000040), "seq_lens_out"), (dict(ws=0), "workspace"), (dict(wsb=15), "workspace"),
+    (dict(lens_out=0x530000000), "seq_lens_out"), (dict(lens_out=0x100000000), "seq_lens_out"),
+    (dict(pos=0x520000002, pout=0x520000002), "4-byte"), (dict(wout=0x530000000, pout=0x720000000), "overlap"), (dict(lens_out=0x510000040), "seq_lens_out"), (dict(ws=0), "workspace"), (dict(wsb=15), "workspace"),
 ])
 def test_evict_rejects(rkv, change, frag):
     assert evict(rkv, cache(rkv), **change) == rkv.RKV_ERR_INVALID_ARG
