@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __gr
     const uint32_t inc = warp_scan(sum);
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    uint32_t above = inc - sum;
-    for (int w = 0; w < warp; ++w) above += warp_sums[w];
+    const uint32_t sums = lane < kSelWarps ? warp_sums[lane] : 0u;
+    uint32_t above = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
     if (above < want && want <= above + sum) {
       for (uint32_t b = 0; b < per; ++b) {
         const uint32_t n = all[top - b];
@@ -441,6 +441,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __gr
     mask |= (n_bins - 1u) << shift;
     want = found[1];
     equal = found[2];
+    if (want == equal) break;   // every key of the bin is kept: its lowest value will do as the bound
   }
 
   // kept: keys above `prefix`, and the first `want` of the `equal` keys at it.
@@ -454,11 +455,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __gr
     __syncthreads();   // warp_sums of an earlier use are read
     if (lane == 0) warp_sums[warp] = mine;
     __syncthreads();
-    uint32_t before = 0, block = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      before += w < warp ? warp_sums[w] : 0u;
-      block += warp_sums[w];
-    }
+    const uint32_t sums = lane < kSelWarps ? warp_sums[lane] : 0u;
+    uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? sums : 0u);
+    const uint32_t block = __reduce_add_sync(0xffffffffu, sums);
     sum = block;
     if (cs > 1) {
       if (tid < cs) ptx::st_cluster(ptx::mapa_shared(ptx::smem_u32(&block_sums[slot][rank]), uint32_t(tid)), block);

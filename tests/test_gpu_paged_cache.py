@@ -141,6 +141,8 @@ def normal_weight(seed):
     ([700], 1, 390, 300, 200, 250),          # more protected than the budget: the first of them stay
     ([1024], 4, 32, 1023, 4, 64),
     ([4097], 2, 1560, 17, 2, 5),
+    ([90, 88], 2, 7, 80, 2, 9),              # scores that do not start on 16-byte boundaries
+    ([2050, 90], 1, 13, 2033, 2, 9),
 ])
 def test_evict(lens, H, P, budget, sinks, recent, in_place):
     need_gpu()

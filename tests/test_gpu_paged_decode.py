@@ -48,6 +48,8 @@ CASES = [
     ([5, 3, 0], 1, 1, 16, 6),          # more queries than tokens
     ([700], 1, 33, 16, 1),             # 33 rows
     ([600], 4, 1, 1560, 1),            # one page, ending far past the length
+    ([40001], 1, 1, 64, 1),            # an item over every block of the launch
+    ([40001], 1, 2, 1560, 2),
 ]
 
 
@@ -297,3 +299,52 @@ def test_largest_rows():
     after = torch.zeros(2, 1, st.cap, device="cuda")
     o = run(st, q, window=40, sinks=2, weight_out=after)
     check_decode(st, q, o, SCALE, 40, 2, None, after.cpu().numpy())
+
+
+def test_window_and_sinks_at_their_largest():
+    need_gpu()
+    st = Streams([5, 900], 2, 16)
+    q = queries(st, 8, 2)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+        o = run(st, q, window=window, sinks=sinks)
+        check_decode(st, q, o, SCALE, window, sinks)
+
+
+def test_two_calls_at_once():
+    # two streams over one cache, each call with its own workspace, again and again
+    need_gpu()
+    from rolling_kv_cache_rope_b200 import rkv
+    st = Streams([3000, 10, 700], 2, 16)
+    qs = [queries(st, 1, 4, seed=s) for s in (1, 2)]
+    devs = [to_dev(q) for q in qs]
+    want = [run(st, q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            outs[i].append(rkv.attn_decode_paged(devs[i], st.cache, st.lens_dev, stream=s))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_calls_in_a_row_without_waiting():
+    # each call reads what the one before wrote (lengths, weights, queries), with nothing in between
+    need_gpu()
+    from rolling_kv_cache_rope_b200 import rkv
+    st = Streams([600, 90], 2, 16)
+    q_bits = queries(st, 1, 2)
+    q = to_dev(q_bits)
+    w, lens = torch.zeros(2, 2, st.cap, device="cuda"), st.lens_dev.clone()
+    ws = torch.empty(rkv.attn_decode_paged_workspace_size(st.cache, 4, 1, True), dtype=torch.uint8, device="cuda")
+    one = torch.zeros_like(w)
+    rkv.attn_decode_paged(q, st.cache, lens, weight_out=one, workspace=ws)
+    o = q
+    for _ in range(20):
+        o = rkv.attn_decode_paged(q, st.cache, lens, weight_in=w, weight_out=w, workspace=ws)
+    want = torch.zeros_like(w)
+    for _ in range(20):
+        want = want + one
+    assert torch.equal(w, want)
+    check_decode(st, q_bits, o, SCALE)

@@ -232,3 +232,11 @@ def test_other_stream_and_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, o3)
+
+
+@pytest.mark.parametrize("off,block,window,sinks", [
+    (2 ** 31 - 1000, 1, 50, 3), (2 ** 31 - 1000, 7, 50, 0), (0, 2 ** 31 - 1, 1, 0), (100, 1, 2 ** 31 - 1, 0),
+    (100, 3, 2, 2 ** 31 - 1), (2 ** 31 - 1000, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1),
+])
+def test_masks_at_their_largest(off, block, window, sinks):
+    run([spec(200, 300, off, window, sinks, block)], 1, 2, (1, 1))
