@@ -85,6 +85,7 @@ constexpr int kVStageBytes = kBN * 64 * 2;     // 16 KB: 128 rows x 64 cols
 constexpr int kThreads = 16 * 32;
 constexpr int kMaxClusters = 128;    // CTA pairs a launch can have (74 on a B200)
 constexpr int kMaxSched = 4096;      // work items a host-built schedule can list
+constexpr int kMaxParts = 128;       // parts of split units in a windowed launch
 constexpr int kTabEntryBytes = 32;   // cos and sin of 4 consecutive rotary pairs
 constexpr int kMaxTabEntries = 768;  // 24 KB of shared memory (cos array, then sin array)
 constexpr float kRescaleLog2 = 8.0f; // move the running max only past 2^8 growth
@@ -142,8 +143,13 @@ struct Params {
   // query heads of one key head that share a unit, 1, 2 or 4: a unit is then
   // 512 / pack rows of each, and its four 128-row sub-tiles belong to `pack`
   // heads, so that a window's tiles serve rows that see nearly the same keys
+  // (a causal window of 1,024 over 16 / 4 heads and 4,097 rows: 70 us, 88
+  // without)
   int32_t pack;
-  uint16_t split_unit[64];   // windowed: the units that run as two items
+  // windowed: items that are parts of a unit, with their entries [kt0, kt1) of
+  // the unit's list of tiles
+  uint16_t part_unit[kMaxParts];
+  int32_t part_kt0[kMaxParts], part_kt1[kMaxParts];
   // work items: units [0, n_whole) whole, then each of the remaining
   // n_split units as two items over the first and second half of its key
   // tiles, whose partial results go to part_o / part_ml
@@ -301,13 +307,13 @@ __device__ __forceinline__ int items_of(const Params& p, int cluster, int n_clus
   if (p.use_sched) return int(p.sched_off[cluster + 1]) - int(p.sched_off[cluster]);
   return cluster < p.total_units ? (p.total_units - cluster + n_clusters - 1) / n_clusters : 0;
 }
-constexpr int kHalfItem = 1 << 30;   // windowed: the item is half of a split unit (0x8000 in the schedule)
+constexpr int kPartItem = 1 << 30;   // windowed: the item is a part of a split unit (0x8000 in the schedule)
 template <bool kWindow>
 __device__ __forceinline__ int item_at(const Params& p, int cluster, int n_clusters, int k) {
   if constexpr (kWindow) {
     if (p.use_sched) {
       const int v = int(p.sched[p.sched_off[cluster] + k]);
-      return v & 0x8000 ? kHalfItem | (v & 0x7FFF) : v;
+      return v & 0x8000 ? kPartItem | (v & 0x7FFF) : v;
     }
     return cluster + k * n_clusters;
   }
@@ -398,9 +404,9 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
   int u = item;
   r.part = -1;
   if constexpr (kWindow) {
-    if (item & kHalfItem) {
-      r.part = item & ~kHalfItem;
-      u = p.split_unit[r.part >> 1];
+    if (item & kPartItem) {
+      r.part = item & ~kPartItem;
+      u = p.part_unit[r.part];
     }
   } else if (item >= p.n_whole) {   // half of a split unit
     r.part = item - p.n_whole;
@@ -431,8 +437,13 @@ __host__ __device__ __forceinline__ Unit decode_unit(const Params& p, int item) 
   r.kt0 = 0;
   r.kt1 = r.nkt;
   if (r.part >= 0) {
-    if (r.part & 1) r.kt0 = r.nkt / 2;
-    else r.kt1 = r.nkt / 2;
+    if constexpr (kWindow) {
+      r.kt0 = p.part_kt0[r.part];
+      r.kt1 = p.part_kt1[r.part];
+    } else {
+      if (r.part & 1) r.kt0 = r.nkt / 2;
+      else r.kt1 = r.nkt / 2;
+    }
   }
   return r;
 }
@@ -1381,7 +1392,6 @@ struct CombineArgs {
   const float* part_o;
   const float2* part_ml;
   int32_t n_split;
-  int32_t pack;   // Params::pack
   CombineUnit unit[kMaxSplit];
 };
 
@@ -1394,8 +1404,7 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   const int rem = int(idx - int64_t(u) * kUnitRows * (kHD / 8));
   const int row = rem / (kHD / 8), cg = rem % (kHD / 8);
   const CombineUnit& cu = a.unit[u];
-  const int sub = row / kBM, rank = sub >> 1, b = sub & 1;
-  const int qrow = cu.row0 + sub_row(a.pack, rank, b) + (row - sub * kBM), head = cu.head + sub_head(a.pack, rank, b);
+  const int qrow = cu.row0 + row;
   if (qrow >= cu.Lq) return;
   const int64_t ra = int64_t(2 * u) * kUnitRows + row, rb = ra + kUnitRows;
   const float2 mla = a.part_ml[ra], mlb = a.part_ml[rb];
@@ -1413,6 +1422,56 @@ __global__ void __launch_bounds__(kCombineThreads) attn_combine_kernel(const __g
   out.y = pack_bf16x2(a0.z * ca + b0.z * cb, a0.w * ca + b0.w * cb);
   out.z = pack_bf16x2(a1.x * ca + b1.x * cb, a1.y * ca + b1.y * cb);
   out.w = pack_bf16x2(a1.z * ca + b1.z * cb, a1.w * ca + b1.w * cb);
+  *reinterpret_cast<uint4*>(cu.o + int64_t(qrow) * cu.o_stride_bytes + int64_t(cu.head) * (kHD * 2) + cg * 16) = out;
+}
+
+// The same for windowed launches, whose split units may have more than two
+// parts and several heads: parts [part0, part0 + parts) of each, in their order.
+struct WindowCombineUnit {
+  uint8_t* o;
+  int64_t o_stride_bytes;
+  int32_t Lq, head, row0, part0, parts, pad;
+};
+struct WindowCombineArgs {
+  const float* part_o;
+  const float2* part_ml;
+  int32_t n_units, pack;
+  WindowCombineUnit unit[kMaxSplit];
+};
+
+__global__ void __launch_bounds__(kCombineThreads) window_combine_kernel(const __grid_constant__ WindowCombineArgs a) {
+  const int64_t idx = int64_t(blockIdx.x) * kCombineThreads + threadIdx.x;   // (unit, row, 8-column group)
+  if (idx >= int64_t(a.n_units) * kUnitRows * (kHD / 8)) return;
+  const int u = int(idx / (kUnitRows * (kHD / 8)));
+  const int rem = int(idx - int64_t(u) * kUnitRows * (kHD / 8));
+  const int row = rem / (kHD / 8), cg = rem % (kHD / 8);
+  const WindowCombineUnit& cu = a.unit[u];
+  const int sub = row / kBM, rank = sub >> 1, b = sub & 1;
+  const int qrow = cu.row0 + sub_row(a.pack, rank, b) + (row - sub * kBM), head = cu.head + sub_head(a.pack, rank, b);
+  if (qrow >= cu.Lq) return;
+  float mx = -INFINITY, lsum = 0.f;
+  for (int i = 0; i < cu.parts; ++i) {
+    const float2 ml = a.part_ml[int64_t(cu.part0 + i) * kUnitRows + row];
+    if (ml.y > 0.f) mx = fmaxf(mx, ml.x);
+  }
+  float acc[8] = {};
+  for (int i = 0; i < cu.parts; ++i) {
+    const int64_t at = int64_t(cu.part0 + i) * kUnitRows + row;
+    const float2 ml = a.part_ml[at];
+    const float w = ml.y > 0.f ? exp2f(ml.x - mx) : 0.f;
+    lsum += ml.y * w;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + at * kHD + cg * 8);
+    const float4 x = src[0], y = src[1];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += v[e] * w;
+  }
+  const float inv = lsum > 0.f ? 1.0f / lsum : 0.f;
+  uint4 out;
+  out.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  out.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+  out.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+  out.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
   *reinterpret_cast<uint4*>(cu.o + int64_t(qrow) * cu.o_stride_bytes + int64_t(head) * (kHD * 2) + cg * 16) = out;
 }
 
@@ -1507,40 +1566,65 @@ static bool build_schedule(Params& p, int64_t units, int max_clusters) {
 }
 
 // Windowed launches: units differ in cost, and there may be few of them.  The
-// longest-first assignment above, with some of the longest units run as two
-// items (halves of their key tiles, merged by attn_combine_kernel) where that
-// shortens the busiest pair's work.  Fills p.use_sched, p.sched_off, p.sched
-// and p.split_unit; returns the number of split units.
-static int build_window_schedule(Params& p, int64_t units, int max_clusters, int max_split) {
+// longest-first assignment above, with the longest units run as several items
+// (runs of their key tiles, merged by window_combine_kernel) where that shortens
+// the busiest pair's work.  Fills p.use_sched, p.sched_off, p.sched and the
+// parts; `split` lists the split units, with their first part and number of
+// parts.  `slots`: partial results the workspace holds.  One head of 4,753 rows
+// over three frames of 30 x 51 takes 69 us (with halves only 115), the denoise
+// pass with a window of four blocks 3.30 ms (unsplit 3.41).
+struct WindowSplit {
+  int n = 0, parts = 0;   // split units, parts of all of them
+  int unit[kMaxSplit], part0[kMaxSplit], count[kMaxSplit];
+};
+static WindowSplit build_window_schedule(Params& p, int64_t units, int max_clusters, int slots) {
+  WindowSplit none, best_split;
   p.use_sched = 0;
-  if (units + kMaxSplit > kMaxSched || max_clusters > kMaxClusters) return 0;
+  if (units + kMaxParts > kMaxSched || max_clusters > kMaxClusters) return none;
+  slots = std::min(slots, kMaxParts);
   struct Item {
     int32_t cost;
     uint16_t code;
   };
   const int n = int(units);
-  std::vector<Item> whole(static_cast<size_t>(n));
+  std::vector<Item> whole(static_cast<size_t>(n)), items;
   for (int u = 0; u < n; ++u) whole[size_t(u)] = {host_unit(p, u).nkt, uint16_t(u)};
-  std::stable_sort(whole.begin(), whole.end(), [](const Item& a, const Item& b) { return a.cost > b.cost; });
-  int most = 0;   // units long enough to be halved
-  while (most < std::min(n, max_split) && whole[size_t(most)].cost >= 4) ++most;
-  // Work of the busiest pair, in key tiles, when the first k units are halved;
-  // an item costs kUnitOverheadTiles beside its tiles, the merge about two
-  std::vector<Item> items;
+  const auto longer = [](const Item& a, const Item& b) { return a.cost > b.cost; };
+  std::stable_sort(whole.begin(), whole.end(), longer);
   std::vector<std::pair<int32_t, int32_t>> heap;   // (work, pair), smallest on top
   std::vector<std::vector<uint16_t>> lists;
-  auto assign = [&](int k, bool keep) {
+  // Work of the busiest pair, in key tiles, when the longest units are cut into
+  // parts of at most `most` tiles (0: none) while slots last; an item costs
+  // kUnitOverheadTiles beside its tiles, the merge about two.  keep: for good.
+  auto assign = [&](int32_t most, bool keep) {
+    WindowSplit s;
     items.clear();
     for (int i = 0; i < n; ++i) {
-      if (i < k) {
-        const int half = whole[size_t(i)].cost / 2;
-        items.push_back({half, uint16_t(0x8000 | (2 * i))});
-        items.push_back({whole[size_t(i)].cost - half, uint16_t(0x8000 | (2 * i + 1))});
-      } else {
-        items.push_back(whole[size_t(i)]);
+      const Item& w = whole[size_t(i)];
+      int k = most > 0 ? (w.cost + most - 1) / most : 1;
+      k = std::min({k, w.cost / 2, slots - s.parts});
+      if (k < 2 || s.n == kMaxSplit) {
+        items.push_back(w);
+        continue;
       }
+      if (keep) {
+        s.unit[s.n] = w.code;
+        s.part0[s.n] = s.parts;
+        s.count[s.n] = k;
+      }
+      for (int j = 0; j < k; ++j) {
+        const int32_t a = int32_t(int64_t(w.cost) * j / k), b = int32_t(int64_t(w.cost) * (j + 1) / k);
+        if (keep) {
+          p.part_unit[s.parts + j] = w.code;
+          p.part_kt0[s.parts + j] = a;
+          p.part_kt1[s.parts + j] = b;
+        }
+        items.push_back({b - a, uint16_t(0x8000 | (s.parts + j))});
+      }
+      s.n++;
+      s.parts += k;
     }
-    if (k > 0) std::stable_sort(items.begin(), items.end(), [](const Item& a, const Item& b) { return a.cost > b.cost; });
+    if (s.parts > 0) std::stable_sort(items.begin(), items.end(), longer);
     const int C = int(std::min<size_t>(items.size(), size_t(max_clusters)));
     heap.clear();
     for (int c = 0; c < C; ++c) heap.push_back({0, c});
@@ -1554,24 +1638,24 @@ static int build_window_schedule(Params& p, int64_t units, int max_clusters, int
       if (keep) lists[size_t(top.second)].push_back(it.code);
       std::push_heap(heap.begin(), heap.end(), std::greater<>());
     }
-    return worst + (k > 0 ? 2 : 0);
+    if (keep) best_split = s;
+    return worst + (s.parts > 0 ? 2 : 0);
   };
-  int best = 0;
-  int32_t least = assign(0, false);
-  for (int q = 1; q <= 4; ++q) {
-    const int k = most * q / 4;
-    if (k == 0) continue;
-    const int32_t work = assign(k, false);
+  int32_t best = 0, least = assign(0, false);
+  // (many units leave few slots for each: halves will do)
+  for (int div : {2, 4, 9, 16}) {
+    const int32_t most = (whole[0].cost + div - 1) / div;
+    if (most < 2 || slots < 2 || (div > 2 && n > 2 * max_clusters)) break;
+    const int32_t work = assign(most, false);
     if (work < least) {
       least = work;
-      best = k;
+      best = most;
     }
   }
   assign(best, true);
-  for (int i = 0; i < best; ++i) p.split_unit[i] = whole[size_t(i)].code;
   // each pair takes its items in the order of the units, head by head, so that
   // the pairs in flight share the K/V tiles of few heads in L2
-  auto unit_of = [&](uint16_t code) { return code & 0x8000 ? p.split_unit[(code & 0x7FFF) >> 1] : code; };
+  auto unit_of = [&](uint16_t code) { return code & 0x8000 ? p.part_unit[code & 0x7FFF] : code; };
   for (auto& list : lists)
     std::stable_sort(list.begin(), list.end(), [&](uint16_t a, uint16_t b) { return unit_of(a) < unit_of(b); });
   int at = 0;
@@ -1581,7 +1665,7 @@ static int build_window_schedule(Params& p, int64_t units, int max_clusters, int
   }
   p.sched_off[lists.size()] = uint16_t(at);
   p.use_sched = 1;
-  return best;
+  return best_split;
 }
 
 static int tail_split_units(int64_t units, int clusters) {
@@ -1745,7 +1829,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
       t_hi = std::max<int64_t>(t_hi, int64_t(s.k_t0) + (s.Lk - 1) / F);
     }
   }
-  if (units >= (windows ? int64_t(kHalfItem) : int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
+  if (units >= (windows ? int64_t(kPartItem) : int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   if (t_lo == INT64_MAX) { t_lo = 0; t_hi = -1; }
   const int64_t n_t = t_hi - t_lo + 1;
   const int32_t pairs[3] = {rope->pairs_t, rope->pairs_h, rope->pairs_w};
@@ -1814,13 +1898,14 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
   // one cost keep round-robin with the tail split below.
   // (attn_fwd_window: a schedule of its own.)
   int n_split = 0;
+  WindowSplit wsplit;
   if (windows) {
-    const size_t room = workspace_bytes > kWorkspaceBytes ? (workspace_bytes - kWorkspaceBytes) / (2 * kPartBytesPerItem) : 0;
+    const size_t room = workspace_bytes > kWorkspaceBytes ? (workspace_bytes - kWorkspaceBytes) / kPartBytesPerItem : 0;
     try {
-      n_split = build_window_schedule(p, units, max_clusters, int(std::min<size_t>(room, kMaxSplit)));
+      wsplit = build_window_schedule(p, units, max_clusters, int(std::min<size_t>(room, kMaxParts)));
     } catch (const std::bad_alloc&) {   // round-robin needs no lists
       p.use_sched = 0;
-      n_split = 0;
+      wsplit = WindowSplit();
     }
   } else {
     // tail split: the last n_split units run as two half-units each when the
@@ -1833,23 +1918,22 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
   CombineArgs ca;
   memset(&ca, 0, sizeof(ca));
   for (int k = 0; k < n_split; ++k) {
-    const int64_t u = windows ? int64_t(p.split_unit[k]) : units - n_split + k;
-    const Unit un = host_unit(p, int(u));
-    if (!windows && un.nkt < 2) { n_split = 0; break; }
+    const Unit un = host_unit(p, int(units - n_split + k));
+    if (un.nkt < 2) { n_split = 0; break; }
     const SeqDev& d = p.seq[un.si];
     ca.unit[k].o = d.o;
     ca.unit[k].o_stride_bytes = d.o_stride_bytes;
     ca.unit[k].Lq = d.Lq;
     ca.unit[k].head = un.head;
-    ca.unit[k].row0 = windows ? un.row0 : un.qb * kUnitRows;
+    ca.unit[k].row0 = un.qb * kUnitRows;
   }
-  ca.pack = p.pack;
+  const int n_parts = windows ? wsplit.parts : 2 * n_split;
   ca.n_split = n_split;
   p.n_whole = int32_t(units - n_split);
   p.n_split = n_split;
-  p.total_units = int32_t(units + n_split);
+  p.total_units = int32_t(units - (windows ? wsplit.n : n_split) + n_parts);   // work items
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWorkspaceBytes);
-  p.part_ml = p.part_o + size_t(2 * n_split) * kUnitRows * kHD;
+  p.part_ml = p.part_o + size_t(n_parts) * kUnitRows * kHD;
   ca.part_o = p.part_o;
   ca.part_ml = reinterpret_cast<const float2*>(p.part_ml);
 
@@ -1871,6 +1955,23 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
     attn_combine_kernel<<<uint32_t((threads + kCombineThreads - 1) / kCombineThreads), kCombineThreads, 0, cs>>>(ca);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "attn_combine_kernel launch");
+  }
+  if (wsplit.n > 0) {
+    WindowCombineArgs wa;
+    memset(&wa, 0, sizeof(wa));
+    wa.part_o = p.part_o;
+    wa.part_ml = reinterpret_cast<const float2*>(p.part_ml);
+    wa.n_units = wsplit.n;
+    wa.pack = p.pack;
+    for (int k = 0; k < wsplit.n; ++k) {
+      const Unit un = host_unit(p, wsplit.unit[k]);
+      const SeqDev& d = p.seq[un.si];
+      wa.unit[k] = {d.o, d.o_stride_bytes, d.Lq, un.head, un.row0, wsplit.part0[k], wsplit.count[k], 0};
+    }
+    const int64_t threads = int64_t(wsplit.n) * kUnitRows * (kHD / 8);
+    window_combine_kernel<<<uint32_t((threads + kCombineThreads - 1) / kCombineThreads), kCombineThreads, 0, cs>>>(wa);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "window_combine_kernel launch");
   }
   return RKV_OK;
 }

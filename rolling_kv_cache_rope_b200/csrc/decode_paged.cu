@@ -747,8 +747,9 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
     cu.c = rec.c;
     load_seq(a, cu);
     const int stride = int(gridDim.y) * (kJoinThreads / 32);
-    int loaded_x0 = -1, loaded_blk = -1;
-    float2 mr = make_float2(0.f, 0.f);   // lane r: maximum and 1 / sum of row r of the row block
+    int loaded_x0 = -1;
+    // lane i: maximum and 1 / sum of rows i and 32 + i of the row block that begins at step loaded_x0
+    float2 mrs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     int skip = int(blockIdx.y) * (kJoinThreads / 32) + warp;
     for (int t = skip; t < rec.n; t += stride) {
       // forward to step t
@@ -786,15 +787,15 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
       for (int blk = 0; blk < a.n_blk; ++blk) {
         const int x0 = rec.first + t - cu.c + blk * cu.nc;   // the item's first step in the whole list
         const int rows_here = min(a.rows - blk * a.rows_tile, a.rows_tile);
-        for (int r0 = 0; r0 < rows_here; r0 += 32) {
-          if (x0 != loaded_x0 || r0 != loaded_blk) {
-            loaded_x0 = x0;
-            loaded_blk = r0;
-            const int r = r0 + lane;
-            mr = make_float2(0.f, 0.f);
+        if (x0 != loaded_x0) {
+          loaded_x0 = x0;
+          const int b0 = split.block_of(x0), n = split.block_of(x0 + cu.nc - 1) - b0 + 1;
+          const int slot = split.first(b0) == x0 ? 0 : 1;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int r = 32 * half + lane;
+            mrs[half] = make_float2(0.f, 0.f);
             if (r < rows_here) {
-              const int b0 = split.block_of(x0), n = split.block_of(x0 + cu.nc - 1) - b0 + 1;
-              const int slot = split.first(b0) == x0 ? 0 : 1;
               float M = -INFINITY, ls = 0.f;
               if (n == 1) {
                 const float2 y = a.item_ml[(int64_t(cu.s) * a.c.H + cu.g) * a.n_blk * a.rows_blk +
@@ -810,9 +811,12 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_
                   M = nm;
                 }
               }
-              if (ls > 0.f) mr = make_float2(M, 1.f / ls);
+              if (ls > 0.f) mrs[half] = make_float2(M, 1.f / ls);
             }
           }
+        }
+        for (int r0 = 0; r0 < rows_here; r0 += 32) {
+          const float2 mr = r0 == 0 ? mrs[0] : mrs[1];
           const float* sc = a.scores + ((int64_t(x0) + cu.c) * a.rows_blk + r0) * a.step_keys + 2 * lane;
           const int rows = min(rows_here - r0, 32);
           int r1 = 0;

@@ -117,8 +117,11 @@ def test_grouped_heads(H, G):
 
 @pytest.mark.parametrize("H,G", [(2, 1), (3, 2), (2, 4), (1, 8)])
 def test_split_units(H, G):
-    # few units of many key tiles run as halves, merged into the output
+    # few units of many key tiles run as several parts, merged into the output
     run([spec(900, 2500, 1600, 1300, 140)], H, G, (1, 1))
+    run([spec(70, 6001, 5931, 5000, 3)], H, G, (1, 1), rows=np.r_[0:3, 40, 67:70])
+    # rows whose window some parts miss altogether
+    run([spec(520, 3000, 2480, 900, 0)], H, G, (1, 1), rows=np.r_[0:4, 127:130, 510:520])
 
 
 def test_windows_with_rope_and_grouped_heads():
