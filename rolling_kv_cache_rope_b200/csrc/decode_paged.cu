@@ -20,12 +20,13 @@
 //
 // Split: the key rows of all (sequence, key head, row block) items, in steps
 // of 64 keys, form one list of T steps, and each of C blocks takes T / C of
-// them in a row: every block gets the same bytes whatever the lengths.  An item that lies in one block is finished there; of the others
-// each block leaves its running maximum, sum and unnormalised O (at most two
-// per block), and a second launch joins them in the order of the keys, so the
-// result does not depend on timing.  Each kernel derives the list from
-// seq_lens itself: nothing is planned on the host, and a captured launch
-// serves growing sequences.
+// them in a row: every block gets the same bytes whatever the lengths.  An
+// item that lies in one block is finished there; of the others each block
+// leaves its running maximum, sum and unnormalised O (at most two per block),
+// and a second launch joins them in the order of the keys, so the result does
+// not depend on timing.  Each kernel derives the list from seq_lens itself:
+// nothing is planned on the host, and a captured launch serves growing
+// sequences.
 //
 // Inside a block: four warps, each with 16 of a step's 64 keys and its own
 // maximum, sum and O in registers, meet only where an item begins or ends.
@@ -34,6 +35,13 @@
 // per SM without registers holding data, across the ends of items too.  A row
 // that is not visible to any query (past the end, outside window and sinks, on
 // a bad page) is not read but zero-filled, so nothing it holds can enter a sum.
+//
+// Measured (GPU time alone): one stream of 32,760 tokens, 12 heads, 42 us for
+// 201 MB; 64 streams of 1 to 8,192 tokens, 32 / 8 heads, 187 us for 1,112 MB
+// (5.9 TB/s).  About 10 us of either do not shrink with the bytes: finding the
+// steps 2, the first copies 3, merging the warps 2, the join 4; and the SMs end
+// 15 to 20% apart, although each reads the same bytes.  With weights (24 streams of
+// 2,000 to 4,097 tokens, 24 / 8 heads, 317 MB): 68.4 us.
 #include <math.h>
 
 #include <algorithm>

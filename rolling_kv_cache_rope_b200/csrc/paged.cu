@@ -88,7 +88,14 @@ static uint64_t score_bytes(const rkv_paged_cache* c) { return uint64_t(c->n_seq
 
 // ---------------------------------------------------------------------------
 // insert: a copy of n_seqs * n_new rows into their places, 16 bytes a thread
-// and step, K and V together; the scores of the new tokens beside it
+// and step, K and V together; the scores of the new tokens beside it.
+//
+// Bound: HBM for many rows, 1 KB read and 1 KB written per token and key head
+// (15,600 tokens of 12 heads, 193 MB counted in K and V read and written: 32.5
+// us, 5.9 TB/s); launch latency for a step's (48 tokens of 8 heads: 3.5 us).
+// A thread takes four pieces of K and of V, all loaded before the first is
+// stored: their page numbers are a load that the loads of the rows do not wait
+// for.
 // ---------------------------------------------------------------------------
 struct InsertArgs {
   CacheDev c;
@@ -155,13 +162,16 @@ __global__ void __launch_bounds__(kInsertThreads) paged_insert_kernel(const __gr
 //   E <= kFew   E rounds of a block-wide minimum over (key, index), about 0.1 us
 //               a round, and the block moves the rows itself: a decode step's
 //               eviction is one launch.  48 streams x 8 heads x 4,096 tokens:
-//               8.6 us for E = 1, 24.6 for E = 16, where the way below takes 31
-//               to 34 for any E
+//               8.5 us for E = 1 (25.6 MB: 3.0 TB/s, the dependent loads of one
+//               head's step bound it), 24.6 for E = 16, where the way below
+//               takes 31 to 34 for any E
 //   otherwise   radix selection of the budget-th largest key, 11 bits a pass,
 //               then lists of the places that fall free and of the tokens that
 //               move into them; a second launch moves the rows over all SMs
-//               (by the selecting blocks themselves 24 heads of 32,760 tokens
-//               cut to 7,800 took 66 us against 59)
+//               (24 heads of 32,760 tokens cut to 7,800: 54.5 us, of them 22
+//               for the selection, a chain of passes, and 21 for the rows,
+//               which move at 6.9 TB/s; by the selecting blocks themselves the
+//               whole took 66 against 58 at that time)
 // A head's tokens are shared out over a cluster of blocks where there are too
 // few heads and sequences to fill the machine; the blocks' histograms and
 // counts meet in distributed shared memory.
@@ -697,7 +707,7 @@ extern "C" rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const in
   a.lens_here = seq_lens_out != seq_lens;
   // blocks a head: one where the heads and sequences alone fill the machine
   // (or a head is short), else up to eight: 24 heads cut from 32,760 to 7,800
-  // tokens take 58 us, with one block each 103
+  // tokens took 58 us, with one block each 103
   const int sms = sm_count();
   a.cluster = 1;
   while (a.cluster < kMaxCluster && items * a.cluster * 2 <= 2 * sms && capacity(cache) >= 2048 * int64_t(a.cluster))
