@@ -1739,9 +1739,11 @@ static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windo
     d.q_frame_offset = s.q_frame_offset; d.block_frames = s.block_frames; d.flags = s.flags;
     if (windows) {
       const rkv_attn_window& w = windows[order[oi]];
-      d.window_blocks = w.window_blocks;
+      // more blocks than the frames below 2^31 make: no window (and every
+      // product with block_tokens stays within 64 bits)
+      d.window_blocks = w.window_blocks > INT32_MAX / s.block_frames ? 0 : w.window_blocks;
       d.block_tokens = int64_t(s.block_frames) * F;
-      d.sink_keys = int32_t(w.sink_blocks < s.Lk ? std::min<int64_t>(s.Lk, w.sink_blocks * d.block_tokens) : s.Lk);
+      d.sink_keys = int32_t(w.sink_blocks > s.Lk / d.block_tokens ? s.Lk : w.sink_blocks * d.block_tokens);
       d.div_block = make_fastdiv(uint32_t(s.block_frames));
     }
     d.n_qblocks = (s.Lq + unit_rows - 1) / unit_rows;   // blocks of rows, one per CTA pair

@@ -501,7 +501,7 @@ def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, str
                 or tuple(s.v.shape[1:]) != (H_kv, D):
             raise ValueError("the sequences of one launch share the numbers of query and key heads")
     arr = (rkv_attn_seq * len(seqs))(*[s.to_c() for s in seqs])
-    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(int(w), int(k)) for w, k in windows])
+    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(_i32(w), _i32(k)) for w, k in windows])
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if workspace is None:
@@ -523,7 +523,7 @@ def attn_window_rows(seqs, windows, H, rope, H_kv=None):
     arr = (rkv_attn_seq * len(seqs))(*[
         rkv_attn_seq(Lq=int(s["Lq"]), Lk=int(s["Lk"]), q_frame_offset=int(s.get("q_frame_offset", 0)),
                      block_frames=int(s["block_frames"])) for s in seqs])
-    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(int(w), int(k)) for w, k in windows])
+    win = (rkv_attn_window * len(seqs))(*[rkv_attn_window(_i32(w), _i32(k)) for w, k in windows])
     lq = [int(s["Lq"]) for s in seqs]
     got = [np.zeros(max(1, sum(lq)), dtype=np.int64) for _ in range(3)]
     units = np.zeros((max(1, sum(int(H) * ((x + 511) // 512) for x in lq)), 4), dtype=np.int32)
@@ -558,6 +558,12 @@ def _elsewhere(index, stream):
     """Whether a call on tensors of device ``index`` has to be made under _on."""
     import torch
     return stream is not None or torch._C._cuda_getDevice() != index
+
+
+def _i32(x):
+    """A count as int32 takes it: one past its range means as much as the
+    largest (ctypes would keep the low 32 bits)."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
 
 
 def _raw_stream(index):
@@ -689,7 +695,7 @@ def attn_decode_paged(q, cache, seq_lens, o=None, window=0, sinks=0, softmax_sca
     workspace, size = cache._workspace(workspace, size)
     _check(_lib.attn_decode_paged(cache.ref, q.data_ptr(), o.data_ptr(), qs, os_, Hq, Lq,
                                   cache._ints(seq_lens, "seq_lens"),
-                                  _SCALE if softmax_scale is None else softmax_scale, window, sinks,
+                                  _SCALE if softmax_scale is None else softmax_scale, _i32(window), _i32(sinks),
                                   cache._scores(weight_in, "weight_in", torch.float32),
                                   cache._scores(weight_out, "weight_out", torch.float32), workspace.data_ptr(), size,
                                   _raw_stream(cache.index)))
@@ -700,7 +706,7 @@ _SCALE = 1.0 / math.sqrt(128)
 
 
 def kvcache_paged_evict_workspace_size(cache, budget):
-    return int(_lib.kvcache_paged_evict_workspace_size(cache.ref, int(budget)))
+    return int(_lib.kvcache_paged_evict_workspace_size(cache.ref, _i32(budget)))
 
 
 def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0, recent=0, seq_lens_out=None,
@@ -720,7 +726,7 @@ def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0,
     size = 0 if workspace is not None else kvcache_paged_evict_workspace_size(cache, budget)
     workspace, size = cache._workspace(workspace, size)
     _check(_lib.kvcache_paged_evict(
-        cache.ref, lens_in, w_in, p_in, cache._ints(next_pos, "next_pos"), budget, sinks, recent,
+        cache.ref, lens_in, w_in, p_in, cache._ints(next_pos, "next_pos"), _i32(budget), _i32(sinks), _i32(recent),
         lens_in if seq_lens_out is None else cache._ints(seq_lens_out, "seq_lens_out"),
         w_in if weight_out is None else cache._scores(weight_out, "weight_out", torch.float32),
         p_in if pos_out is None else cache._scores(pos_out, "pos_out", torch.int32), workspace.data_ptr(), size,

@@ -118,3 +118,21 @@ def test_window_rows_rejects(rkv):
         rkv.attn_window_rows([dict(Lq=1, Lk=1, block_frames=0)], [(1, 1)], 1, rkv.make_rope(1, 1))
     with pytest.raises(rkv.RkvError, match="window_blocks"):
         rkv.attn_window_rows([dict(Lq=1, Lk=1, block_frames=1)], [(-2, 1)], 1, rkv.make_rope(1, 1))
+
+
+@pytest.mark.parametrize("block,window,sinks", [(2 ** 30, 2 ** 31 - 1, 0), (2 ** 30, 2 ** 31 - 1, 2 ** 31 - 1),
+                                                (1, 2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1, 4), (1, 2 ** 40 + 1, 2 ** 40)])
+def test_window_past_everything(rkv, block, window, sinks):
+    """Windows, blocks and sinks whose products pass 64 bits see all that the block mask leaves."""
+    seqs = [dict(Lq=1000, Lk=9000, block_frames=block, q_frame_offset=3)]
+    got = rkv.attn_window_rows(seqs, [(window, sinks)], 1, rkv.make_rope(30, 52))
+    ref = rkv.attn_window_rows(seqs, [(0, 0)], 1, rkv.make_rope(30, 52))
+    assert (np.asarray(got[1][0]) == 0).all()
+    assert (np.asarray(got[2][0]) == np.asarray(ref[2][0])).all()
+
+
+def test_sinks_past_64_bits(rkv):
+    """2^14 first blocks of 2^30 frames of 2^20 tokens: every key up to the row's limit."""
+    seqs = [dict(Lq=20, Lk=50000, block_frames=2 ** 30)]
+    sink, _, limit, _ = rkv.attn_window_rows(seqs, [(1, 2 ** 14)], 1, rkv.make_rope(2 ** 10, 2 ** 10))
+    assert (np.asarray(sink[0]) == 50000).all() and (np.asarray(limit[0]) == 50000).all()
