@@ -582,7 +582,9 @@ int32_t rkv_ring_slot(const rkv_ring* ring, int32_t logical_frame);
  *                  may share pages that are only read.
  *   status         device int32 the calls below record device-side findings
  *                  in (rkv_paged_status), zeroed by the caller once; or NULL
- * A sequence's capacity is max_pages * page_tokens tokens.
+ * A sequence's capacity is max_pages * page_tokens tokens, below 2^30; the
+ * pool holds fewer than 2^32 head rows, a page fewer than 2^31, and
+ * n_seqs * H is below 2^28 (otherwise RKV_ERR_UNSUPPORTED).
  *
  * Lengths are on the device, so one captured launch serves a growing stream:
  *   seq_lens       device int32 [n_seqs], tokens of each sequence, those a
@@ -698,7 +700,8 @@ rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void* q, void* 
  *                  kvcache_paged_evict_workspace_size(cache, budget) bytes
  * A sequence whose pages hold tokens outside the pool keeps those tokens'
  * rows unmoved (status records it).  Sequences must not share pages.
- * Errors: RKV_ERR_INVALID_ARG (cache, pointers, overlap, sizes, workspace).
+ * Errors: RKV_ERR_INVALID_ARG (cache, pointers, overlap, sizes, workspace),
+ * RKV_ERR_UNSUPPORTED (2^24 or more sequences times key heads).
  */
 size_t kvcache_paged_evict_workspace_size(const rkv_paged_cache* cache, int32_t budget);
 rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const int32_t* seq_lens, const float* weight,

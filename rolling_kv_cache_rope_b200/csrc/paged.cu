@@ -60,6 +60,9 @@ rkv_status check_cache(const rkv_paged_cache* c) {
   if (c->page_stride % kHD) return fail(RKV_ERR_INVALID_ARG, "cache page_stride must be a multiple of D");
   if (c->page_stride / kHD >= (int64_t(1) << 32) / c->n_pages)
     return fail(RKV_ERR_UNSUPPORTED, "the pool holds 2^32 or more head rows");
+  // (the calls' 64-bit counts of rows, pieces and score bytes start from these)
+  if (int64_t(c->n_seqs) * c->H >= (int64_t(1) << 28))
+    return fail(RKV_ERR_UNSUPPORTED, "2^28 or more key heads of all sequences");
   if (capacity(c) >= (int64_t(1) << 30)) return fail(RKV_ERR_UNSUPPORTED, "a sequence's capacity is 2^30 tokens or more");
   if (rows_overlap(c->k, c->n_pages, c->page_stride * 2, page_bytes(c), c->v, c->n_pages, c->page_stride * 2,
                    page_bytes(c)))

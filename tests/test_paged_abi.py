@@ -162,3 +162,12 @@ def test_python_cache_refuses_host_tensors(rkv):
     k = torch.zeros(4, 8, 2, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         rkv.PagedKVCache(k, k.clone(), torch.zeros(1, 2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("call", [insert, decode, evict])
+def test_counts_past_64_bits(rkv, call):
+    """2^30 key heads times 2^30 sequences: products of the counts would wrap around."""
+    c = cache(rkv, H=1 << 30, n_seqs=1 << 30, page_tokens=1, n_pages=1, page_stride=128 << 30, max_pages=1,
+              table_stride=1, k=1 << 52, v=1 << 53)
+    assert call(rkv, c) == rkv.RKV_ERR_UNSUPPORTED
+    assert "2^28" in rkv.rkv_last_error_string()
