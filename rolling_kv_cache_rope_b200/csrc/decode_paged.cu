@@ -19,7 +19,7 @@
 // this bandwidth (16 keys of a head cost 32 of them per 8 KB).
 //
 // Split: the key rows of all (sequence, key head, row block) items, in steps
-// of 64 keys, form one list of T steps, and each of C blocks takes T / C of
+// of 64 or 32 keys, form one list of T steps, and each of C blocks takes T / C of
 // them in a row: every block gets the same bytes whatever the lengths.  An
 // item that lies in one block is finished there; of the others each block
 // leaves its running maximum, sum and unnormalised O (at most two per block),
@@ -28,7 +28,8 @@
 // nothing is planned on the host, and a captured launch serves growing
 // sequences.
 //
-// Inside a block: four warps, each with 16 of a step's 64 keys and its own
+// Inside a block: four warps, each with 16 of a step's 64 keys (more rows than
+// 16: two or four warps share 32 keys, 16 rows each) and its own
 // maximum, sum and O in registers, meet only where an item begins or ends.
 // Each warp copies its own K and V rows with 16-byte asynchronous copies into
 // its part of a ring of stages, so several steps (32 KB each) are in flight
@@ -41,7 +42,7 @@
 // (5.9 TB/s).  About 10 us of either do not shrink with the bytes: finding the
 // steps 2, the first copies 3, merging the warps 2, the join 4; and the SMs end
 // 15 to 20% apart, although each reads the same bytes.  With weights (24 streams of
-// 2,000 to 4,097 tokens, 24 / 8 heads, 317 MB): 68.4 us.
+// 2,000 to 4,097 tokens, 24 / 8 heads, 317 MB): 68.6 us.
 #include <math.h>
 
 #include <algorithm>
@@ -56,8 +57,8 @@ namespace paged {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kDecPerSm = 2;                           // blocks of the main launch an SM holds
-constexpr int kTileKeys = 16;                          // keys a warp takes at a time
-constexpr int kTileBytes = kTileKeys * int(kRowBytes); // 4 KB of K, as much of V
+constexpr int kGroupKeys = 16;                         // keys of one matrix product
+constexpr int kGroupBytes = kGroupKeys * int(kRowBytes);
 constexpr int kRingBytes = 96 * 1024;                  // K and V stages of a block
 constexpr float kMaxSlack = 8.0f;                      // the running maximum moves past 2^8 growth only
 constexpr int kMaxRows = 4096;                         // query rows of a key head (Lq * G)
@@ -80,7 +81,7 @@ struct DecodeArgs {
   int32_t Hq, Lq, G, rows;       // rows = Lq * G
   FastDiv div_G;
   int32_t rows_tile;             // rows a row block has room for: 16, 32 or 64
-  int32_t step_keys;             // keys of a step: 64, 32 or 16
+  int32_t step_keys;             // keys of a step: 64 or 32
   int32_t rows_blk, n_blk;       // rows of a full row block (min(rows, rows_tile)), row blocks
   int32_t window, sinks;
   int32_t main_blocks;           // C
@@ -196,10 +197,18 @@ __device__ __forceinline__ void advance(const DecodeArgs& a, Cursor& u) {
 __device__ __forceinline__ int token_of(const Span& sp, int x) { return x < sp.se ? x : x - sp.se + sp.lo; }
 
 // Shared memory of a block whose warps split into NR row tiles: 4 / NR key
-// tiles of 16 keys a step, each read by NR warps.
+// tiles a step, each read by NR warps.  A tile is 16 keys, or two groups of 16
+// where warps share it: they then meet, and form addresses and masks, half as
+// often, and two chains of products run side by side (16 streams of 8,000
+// tokens, 4 key heads: 32 rows 61 us, 73 with one group; 64 rows 93, 121).
+// With one row tile HBM is the bound, and smaller tiles keep more steps in
+// flight.
 template <int NR>
 struct DecSmem {
   static constexpr int kKeyTiles = kDecWarps / NR;
+  static constexpr int kGroups = NR == 1 ? 1 : 2;
+  static constexpr int kTileKeys = kGroups * kGroupKeys;
+  static constexpr int kTileBytes = kGroups * kGroupBytes;   // of K, and of V
   static constexpr int kStepKeys = kKeyTiles * kTileKeys;
   static constexpr int kStageBytes = kKeyTiles * 2 * kTileBytes;
   static constexpr int kStages = kRingBytes / kStageBytes;
@@ -216,6 +225,7 @@ template <int NR, bool kWeights>
 __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(const __grid_constant__ DecodeArgs a) {
   using SM = DecSmem<NR>;
   constexpr int kStages = SM::kStages, kKeyTiles = SM::kKeyTiles;
+  constexpr int kGroups = SM::kGroups, kTileKeys = SM::kTileKeys, kTileBytes = SM::kTileBytes;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = ptx::smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -265,8 +275,9 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
     // p of row r at place p ^ (r % 8), so that eight rows' pieces of one
     // column block fall into different banks.  Of the places a lane touches
     // only four differ beyond a constant: x ^ 2c for c = 0..3.
-    constexpr int kCopies = 8 / NR;                          // row pairs of a tile this warp copies
+    constexpr int kCopies = kTileKeys / NR / 2;             // row pairs of a tile this warp copies
     constexpr int kDistinct = kCopies < 4 ? kCopies : 4;
+    constexpr uint32_t kAllKeys = kTileKeys == 32 ? 0xFFFFFFFFu : (1u << (kTileKeys & 31)) - 1u;
     uint32_t dofs[kDistinct], kofs[4], vofs[4];
     {
       const uint32_t hi = uint32_t(lane) >> 4, low = uint32_t(lane) & 7u, piece = uint32_t(lane) & 15u;
@@ -291,7 +302,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
     // Copy this warp's share of its key tile of step `is` into its stage.
     auto issue = [&]() {
       if (issued < n_steps) {
-        const int x0 = is.c * SM::kStepKeys + kt * kTileKeys, x = x0 + (lane & 15);
+        const int x0 = is.c * SM::kStepKeys + kt * kTileKeys, x = x0 + (lane & (kTileKeys - 1));
         if (x0 < is.sp.span) {   // a tile past the list's end is not computed either
           bool ok = x < is.sp.span;
           uint32_t unit = 0;
@@ -303,7 +314,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
             unit = page * a.c.page_units + (j - pg * a.c.P) * uint32_t(a.c.H) + uint32_t(is.g);
             if (!ok) record(a.c, kBadPage);
           }
-          const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
+          const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kAllKeys;
           if (lane == 0) vmask[st_is * kDecWarps + warp] = mask;
           const uint32_t so = st_is * SM::kStageBytes;
           const int kk0 = rt * (kTileKeys / NR) + (lane >> 4);
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
               constexpr int kOff = (i / 4) * 8 * int(kRowBytes);   // rows 8 apart swizzle alike
               const uint32_t d = dofs[i % kDistinct] + so;
               const uint64_t off = uint64_t(__shfl_sync(0xffffffffu, unit, kk0 + 2 * i)) * kRowBytes;
-              if (mask == 0xFFFFu) {
+              if (mask == kAllKeys) {
                 ptx::cp_async16<kOff>(d, k_lane + off);
                 ptx::cp_async16<kOff + kTileBytes>(d, v_lane + off);
               } else {   // rows that are not there are zeros
@@ -398,10 +409,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
       if (x0 < cu.sp.span) {
         const uint32_t mask = vmask[st * kDecWarps + warp];
         const uint32_t so = st * SM::kStageBytes;
-        // S = Q K^T, 16 rows x 16 keys
-        float S[2][4];
+        // S = Q K^T, 16 rows x 16 or 32 keys, eight to an accumulator
+        constexpr int kCols = 2 * kGroups;
+        float S[kCols][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kCols; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
         auto s_step = [&](auto kc) {
@@ -410,6 +422,11 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
           ptx::ldsm4<(kk >> 2) * 128>(kofs[kk & 3] + so, b);
           ptx::mma_bf16(S[0], qf[kk], b[0], b[1]);
           ptx::mma_bf16(S[1], qf[kk], b[2], b[3]);
+          if constexpr (kGroups == 2) {
+            ptx::ldsm4<(kk >> 2) * 128 + kGroupBytes>(kofs[kk & 3] + so, b);
+            ptx::mma_bf16(S[kCols - 2], qf[kk], b[0], b[1]);
+            ptx::mma_bf16(S[kCols - 1], qf[kk], b[2], b[3]);
+          }
         };
         s_step(std::integral_constant<int, 0>());
         s_step(std::integral_constant<int, 1>());
@@ -419,10 +436,10 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
         s_step(std::integral_constant<int, 5>());
         s_step(std::integral_constant<int, 6>());
         s_step(std::integral_constant<int, 7>());
-        // the tile holds tokens j0 .. j0 + 15 unless the list jumps from the
+        // the tile holds the tokens from j0 on unless the list jumps from the
         // sinks to the window inside it; no mask is needed where every row sees all
         const int j0 = token_of(cu.sp, x0);
-        const bool plain = mask == 0xFFFFu && (x0 >= cu.sp.se || x0 + kTileKeys <= cu.sp.se) &&
+        const bool plain = mask == kAllKeys && (x0 >= cu.sp.se || x0 + kTileKeys <= cu.sp.se) &&
                            j0 + kTileKeys <= all_hi && (j0 >= all_lo || j0 + kTileKeys <= a.sinks);
         if (!plain) {
 #pragma unroll
@@ -432,7 +449,7 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
             const int c = row < a.rows ? cu.sp.L - a.Lq + int(fdiv(uint32_t(row), a.div_G)) : -1;
             const int from = a.window > 0 ? c - a.window + 1 : 0;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kCols; ++n)
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
                 const int kk = n * 8 + 2 * (lane & 3) + f;
@@ -449,18 +466,24 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
             const int r = rt * 16 + e * 8 + (lane >> 2);
             if (r < a.rows_blk) {
               float* dst = a.scores + (step * a.rows_blk + r) * SM::kStepKeys + kt * kTileKeys + 2 * (lane & 3);
-              *reinterpret_cast<float2*>(dst) = make_float2(S[0][2 * e] * a.scale_log2, S[0][2 * e + 1] * a.scale_log2);
-              *reinterpret_cast<float2*>(dst + 8) =
-                  make_float2(S[1][2 * e] * a.scale_log2, S[1][2 * e + 1] * a.scale_log2);
+#pragma unroll
+              for (int n = 0; n < kCols; ++n)
+                *reinterpret_cast<float2*>(dst + 8 * n) =
+                    make_float2(S[n][2 * e] * a.scale_log2, S[n][2 * e + 1] * a.scale_log2);
             }
           }
         }
-        // a lane sees four of a row's sixteen scores; only where one of them
+        // a lane sees a quarter of a row's scores; only where one of them
         // outgrows the running maximum do the row's lanes find the tile's
         float mx[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          mx[e] = a.scale_log2 * fmaxf(fmaxf(S[0][2 * e], S[0][2 * e + 1]), fmaxf(S[1][2 * e], S[1][2 * e + 1]));
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(fmaxf(S[0][2 * e], S[0][2 * e + 1]), fmaxf(S[1][2 * e], S[1][2 * e + 1]));
+          if constexpr (kGroups == 2)
+            mx[e] = fmaxf(mx[e], fmaxf(fmaxf(S[kCols - 2][2 * e], S[kCols - 2][2 * e + 1]),
+                                       fmaxf(S[kCols - 1][2 * e], S[kCols - 1][2 * e + 1])));
+          mx[e] *= a.scale_log2;
+        }
         if (__any_sync(0xffffffffu, mx[0] > m[0] + kMaxSlack || mx[1] > m[1] + kMaxSlack)) {
           float f[2];
 #pragma unroll
@@ -483,26 +506,31 @@ __global__ void __launch_bounds__(kDecThreads, kDecPerSm) decode_paged_kernel(co
         // P = exp2(S - m): summed in fp32, rounded to bf16 for P V (at most
         // half a step of bf16, 2^-8 of each weight, as the output's own
         // rounding).  S's accumulator layout is the A operand's as it stands.
-        uint32_t P[4];
+        uint32_t P[kGroups][4];
         const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kCols; ++n) {
           const float p0 = ptx::ex2_approx(fmaf(S[n][0], a.scale_log2, -u0));
           const float p1 = ptx::ex2_approx(fmaf(S[n][1], a.scale_log2, -u0));
           const float p2 = ptx::ex2_approx(fmaf(S[n][2], a.scale_log2, -u1));
           const float p3 = ptx::ex2_approx(fmaf(S[n][3], a.scale_log2, -u1));
           l[0] += p0 + p1;
           l[1] += p2 + p3;
-          P[2 * n] = pack_bf16x2(p0, p1);
-          P[2 * n + 1] = pack_bf16x2(p2, p3);
+          P[n / 2][2 * (n & 1)] = pack_bf16x2(p0, p1);
+          P[n / 2][2 * (n & 1) + 1] = pack_bf16x2(p2, p3);
         }
         // O += P V
         auto o_step = [&](auto nc) {
           constexpr int np = decltype(nc)::value;
           uint32_t b[4];   // keys 0-7 / 8-15 of columns 16np.., then of 16np + 8..
           ptx::ldsm4_trans<(np >> 2) * 128>(vofs[np & 3] + so, b);
-          ptx::mma_bf16(O[2 * np], P, b[0], b[1]);
-          ptx::mma_bf16(O[2 * np + 1], P, b[2], b[3]);
+          ptx::mma_bf16(O[2 * np], P[0], b[0], b[1]);
+          ptx::mma_bf16(O[2 * np + 1], P[0], b[2], b[3]);
+          if constexpr (kGroups == 2) {
+            ptx::ldsm4_trans<(np >> 2) * 128 + kGroupBytes>(vofs[np & 3] + so, b);
+            ptx::mma_bf16(O[2 * np], P[kGroups - 1], b[0], b[1]);
+            ptx::mma_bf16(O[2 * np + 1], P[kGroups - 1], b[2], b[3]);
+          }
         };
         o_step(std::integral_constant<int, 0>());
         o_step(std::integral_constant<int, 1>());
@@ -632,8 +660,11 @@ __device__ __forceinline__ int64_t part_row(const DecodeArgs& a, int b0, int slo
   return (int64_t(b0 + i) * 2 + (i == 0 ? slot : 0)) * a.rows_blk + r;
 }
 
+// (blocks per SM: without weights the parts of many rows want four, 50 us
+// against 52 for four query tokens of 16 streams; with weights 64 registers
+// spill, 71.1 us against 68.6)
 template <bool kWeights>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, kWeights ? 3 : 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float4 part[kJoinThreads / 32][32];
   __shared__ float2 part_sum[kJoinThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -878,10 +909,12 @@ static rkv_status decode_shape(const rkv_paged_cache* c, int32_t Hq, int32_t Lq,
   if (d.rows > kMaxRows) return fail(RKV_ERR_UNSUPPORTED, "more than %d query rows to a key head", kMaxRows);
   // A row block is as many 16-row tiles as the rows need, up to the four that a
   // block's warps can take: K and V are read once for all of them.  16 streams
-  // of 8,000 tokens, 4 key heads: 32 rows 73 us (in blocks of 16 rows 94), 64
-  // rows 120 (in blocks of 32 rows 122), 128 rows 212 (223)
+  // of 8,000 tokens, 4 key heads: 16 rows 55 us, 32 rows 61 (in two blocks of
+  // 16 rows 94), 64 rows 93, 128 rows 155
   d.rows_tile = d.rows <= 16 ? 16 : (d.rows <= 32 ? 32 : 64);
-  d.step_keys = 1024 / d.rows_tile;
+  d.step_keys = d.rows_tile == 16   ? DecSmem<1>::kStepKeys
+                : d.rows_tile == 32 ? DecSmem<2>::kStepKeys
+                                    : DecSmem<4>::kStepKeys;
   d.rows_blk = std::min(d.rows, d.rows_tile);
   d.n_blk = (d.rows + d.rows_tile - 1) / d.rows_tile;
   d.items = int64_t(c->n_seqs) * c->H * d.n_blk;
