@@ -703,8 +703,9 @@ rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void* q, void* 
  *   budget         >= 1, sinks, recent >= 0
  *   workspace      as for attn_decode_paged,
  *                  kvcache_paged_evict_workspace_size(cache, budget) bytes
- * A sequence whose pages hold tokens outside the pool keeps those tokens'
- * rows unmoved (status records it).  Sequences must not share pages.
+ * A move from or to a token on a page outside the pool is left out whole: the
+ * place keeps its K and V rows, weight and pos, and status records it.
+ * Sequences must not share pages.
  * Errors: RKV_ERR_INVALID_ARG (cache, pointers, overlap, sizes, workspace),
  * RKV_ERR_UNSUPPORTED (2^24 or more sequences times key heads).
  */

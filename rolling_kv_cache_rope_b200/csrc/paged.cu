@@ -379,11 +379,11 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __gr
         uint8_t* pool = (lane < 16 ? a.c.k : a.c.v) + (lane & 15) * 16;
         *reinterpret_cast<uint4*>(pool + uint64_t(row_unit(a.c, pd, uint32_t(to), h)) * kRowBytes) =
             *reinterpret_cast<const uint4*>(pool + uint64_t(row_unit(a.c, ps, uint32_t(from), h)) * kRowBytes);
-      } else {
+        if (lane == 0) weight_out[to] = weight[from];   // from >= budget > to
+        if (lane == 1) pos_out[to] = pos[from];
+      } else {   // no move at all: a row keeps its own scores
         record(a.c, kBadPage);
       }
-      if (lane == 0) weight_out[to] = weight[from];   // from >= budget > to
-      if (lane == 1) pos_out[to] = pos[from];
     }
     return;
   }
@@ -530,12 +530,16 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const __gr
   if (tid == 0 && rank == 0) a.count[item] = int(total);
   for (int i = rank * kSelThreads + tid; i < int(total); i += cs * kSelThreads) {
     const int from = src[i], to = dst[i];
-    weight_out[to] = weight[from];   // from >= budget > to: no index is both read and written
-    pos_out[to] = pos[from];
-    // the second launch gets the rows themselves (equal ones: nothing to move)
+    // the second launch gets the rows themselves (equal ones: no move at all, a
+    // row keeps its own scores)
     const uint32_t ps = page_of(a.c, s, uint32_t(from)), pd = page_of(a.c, s, uint32_t(to));
     const bool ok = ps < a.c.n_pages && pd < a.c.n_pages;
-    if (!ok) record(a.c, kBadPage);
+    if (ok) {
+      weight_out[to] = weight[from];   // from >= budget > to: no index is both read and written
+      pos_out[to] = pos[from];
+    } else {
+      record(a.c, kBadPage);
+    }
     src[i] = ok ? int32_t(row_unit(a.c, ps, uint32_t(from), h)) : 0;
     dst[i] = ok ? int32_t(row_unit(a.c, pd, uint32_t(to), h)) : 0;
   }
