@@ -636,6 +636,7 @@ typedef struct {
  *                  next_pos[s] - n_new + i, next_pos with the new tokens
  *                  included
  *   weight         optional: weight[s][h][token] = 0
+ * A token on a page outside the pool gets neither row nor scores.
  * Two sequences must not insert into the same page.
  * Errors: RKV_ERR_INVALID_ARG (cache, pointers, strides, overlap, n_new < 0 or
  * above the capacity), RKV_ERR_UNSUPPORTED (2^31 or more 16-byte pieces).

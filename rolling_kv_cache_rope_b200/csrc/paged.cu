@@ -135,16 +135,16 @@ __global__ void __launch_bounds__(kInsertThreads) paged_insert_kernel(const __gr
     vv[u] = *reinterpret_cast<const uint4*>(a.v_new + src);
     const int j = seq_len(a.c, a.seq_lens, int(s)) - a.n_new + int(i);
     if (j < 0) continue;
+    const uint32_t page = page_of(a.c, int(s), uint32_t(j));
+    if (page >= a.c.n_pages) {   // no such token: its scores are left as well
+      record(a.c, kBadPage);
+      continue;
+    }
     const uint32_t h = piece >> 4;
     if ((piece & 15u) == 0) {
       const int64_t at = (int64_t(s) * a.c.H + h) * a.c.capacity + j;
       if (a.pos) a.pos[at] = a.next_pos[s] - a.n_new + int(i);
       if (a.weight) a.weight[at] = 0.f;
-    }
-    const uint32_t page = page_of(a.c, int(s), uint32_t(j));
-    if (page >= a.c.n_pages) {
-      record(a.c, kBadPage);
-      continue;
     }
     dst[u] = uint64_t(row_unit(a.c, page, uint32_t(j), int(h))) * kRowBytes + (piece & 15u) * 16u;
   }

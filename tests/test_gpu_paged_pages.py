@@ -69,3 +69,33 @@ def test_evict_moves_rows_and_scores_together(lens, H, P, budget, bad, in_place)
     assert torch.equal(bits(st.cache.k), k0) and torch.equal(bits(st.cache.v), v0)
     assert np.array_equal(got_p.cpu().numpy(), want_p)
     assert np.array_equal(got_w.cpu().numpy(), want_w)
+
+
+@pytest.mark.parametrize("lens,H,P,new", [([40, 9], 2, 16, 1), ([40, 9], 3, 4, 12), ([500], 12, 16, 33)])
+def test_insert_leaves_scores_of_tokens_without_a_page(lens, H, P, new):
+    need_gpu()
+    from rolling_kv_cache_rope_b200 import rkv
+    st = Streams(lens, H, P, seed=22)
+    n, L = st.n, lens[0]
+    bad = (L - 1) // P            # the page of the first stream's newest token
+    st.cache.page_table[0, bad] = st.cache.k.shape[0]
+    kb, vb = bf16_normal_bits(50, (n * new, H, D)), bf16_normal_bits(51, (n * new, H, D))
+    k0, v0 = bits(st.cache.k).clone(), bits(st.cache.v).clone()
+    pos = torch.full((n, H, st.cap), -1, dtype=torch.int32, device="cuda")
+    weight = torch.full((n, H, st.cap), 2.5, device="cuda")
+    rkv.kvcache_paged_insert(st.cache, to_dev(kb), to_dev(vb), st.lens_dev, next_pos=st.lens_dev + 500, pos=pos, weight=weight)
+    with pytest.raises(rkv.RkvError, match="page"):
+        rkv.rkv_paged_status(st.cache)
+    want_p, want_w = np.full(pos.shape, -1), np.full(weight.shape, 2.5)
+    for s, x in enumerate(lens):
+        pg, tk = st.rows(s)
+        for i in range(new):
+            j = x - new + i
+            if j < 0 or (s == 0 and j // P == bad):
+                continue
+            for t, src in ((k0, kb), (v0, vb)):
+                t[pg[j], tk[j]] = torch.from_numpy(src[s * new + i].view(np.int16)).cuda()
+            want_p[s, :, j], want_w[s, :, j] = x + 500 - new + i, 0.0
+    assert torch.equal(bits(st.cache.k), k0) and torch.equal(bits(st.cache.v), v0)
+    assert np.array_equal(pos.cpu().numpy(), want_p)
+    assert np.array_equal(weight.cpu().numpy(), want_w)
