@@ -590,6 +590,7 @@ int32_t rkv_ring_slot(const rkv_ring* ring, int32_t logical_frame);
  * A sequence's capacity is max_pages * page_tokens tokens, below 2^30; the
  * pool holds fewer than 2^32 head rows, a page fewer than 2^31, and
  * n_seqs * H is below 2^28 (otherwise RKV_ERR_UNSUPPORTED).
+ * table_stride is below 2^32 where there are several sequences.
  *
  * Lengths are on the device, so one captured launch serves a growing stream:
  *   seq_lens       device int32 [n_seqs], tokens of each sequence, those a

@@ -980,16 +980,16 @@ extern "C" rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void
   if (!aligned16(q) || !aligned16(o)) return fail(RKV_ERR_INVALID_ARG, "q/o must be 16-byte aligned");
   if (!aligned4(seq_lens) || !aligned4(weight_in) || !aligned4(weight_out))
     return fail(RKV_ERR_INVALID_ARG, "seq_lens/weight_in/weight_out must be 4-byte aligned");
-  const int64_t row = int64_t(Hq) * kHD;
+  const int64_t row = int64_t(Hq) * kHD, n_rows = int64_t(cache->n_seqs) * Lq;
   for (int64_t stride : {q_row_stride, o_row_stride}) {
     if (stride < row) return fail(RKV_ERR_INVALID_ARG, "row stride < Hq*D");
     if (stride % 8) return fail(RKV_ERR_INVALID_ARG, "rows of q/o must be 16-byte aligned");
-    if (stride >= (int64_t(1) << 40)) return fail(RKV_ERR_INVALID_ARG, "row stride too large");
+    if (stride >= (int64_t(1) << 40) || stride >= kMaxSpan / n_rows)
+      return fail(RKV_ERR_INVALID_ARG, "row stride too large");
   }
   if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return fail(RKV_ERR_INVALID_ARG, "softmax_scale must be > 0");
   if (window < 0 || sinks < 0) return fail(RKV_ERR_INVALID_ARG, "window and sinks must be >= 0");
   if (weight_in && !weight_out) return fail(RKV_ERR_INVALID_ARG, "weight_in without weight_out");
-  const int64_t n_rows = int64_t(cache->n_seqs) * Lq;
   if (rows_overlap(o, n_rows, o_row_stride * 2, row * 2, q, n_rows, q_row_stride * 2, row * 2))
     return fail(RKV_ERR_INVALID_ARG, "o overlaps q");
   const uint64_t o_bytes = uint64_t((n_rows - 1) * o_row_stride + row) * 2;

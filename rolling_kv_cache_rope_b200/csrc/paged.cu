@@ -50,6 +50,8 @@ rkv_status check_cache(const rkv_paged_cache* c) {
   if (c->n_pages < 1 || c->page_tokens < 1 || c->H < 1 || c->n_seqs < 1 || c->max_pages < 1)
     return fail(RKV_ERR_INVALID_ARG, "cache n_pages/page_tokens/H/n_seqs/max_pages must be >= 1");
   if (c->table_stride < c->max_pages) return fail(RKV_ERR_INVALID_ARG, "cache table_stride < max_pages");
+  if (c->n_seqs > 1 && c->table_stride >= (int64_t(1) << 32))
+    return fail(RKV_ERR_INVALID_ARG, "cache table_stride too large");
   if (!aligned16(c->k) || !aligned16(c->v)) return fail(RKV_ERR_INVALID_ARG, "cache pools must be 16-byte aligned");
   if (!aligned4(c->page_table) || !aligned4(c->status))
     return fail(RKV_ERR_INVALID_ARG, "cache page_table/status must be 4-byte aligned");
@@ -613,6 +615,7 @@ extern "C" rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const v
   if (new_row_stride % 8) return fail(RKV_ERR_INVALID_ARG, "rows of k_new/v_new must be 16-byte aligned");
   if (new_row_stride >= (int64_t(1) << 40)) return fail(RKV_ERR_INVALID_ARG, "new_row_stride too large");
   const int64_t rows = int64_t(cache->n_seqs) * n_new;
+  if (new_row_stride >= kMaxSpan / rows) return fail(RKV_ERR_INVALID_ARG, "new_row_stride too large for the rows");
   const int64_t pieces = rows * cache->H * 16;
   if (rows >= (int64_t(1) << 31) || pieces >= (int64_t(1) << 31) - kInsertThreads * kInsertUnroll)
     return fail(RKV_ERR_UNSUPPORTED, "insert too large for one launch");

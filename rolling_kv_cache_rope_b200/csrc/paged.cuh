@@ -12,6 +12,7 @@ namespace paged {
 
 constexpr int kHD = 128;                  // head dim
 constexpr uint32_t kRowBytes = kHD * 2;   // one token of one key head: the unit rows are counted in
+constexpr int64_t kMaxSpan = int64_t(1) << 58;   // elements from a tensor's first row to its last: bytes stay within 64 bits
 
 struct CacheDev {
   uint8_t* k;
