@@ -601,6 +601,11 @@ int32_t rkv_ring_slot(const rkv_ring* ring, int32_t logical_frame);
  * a page outside [0, n_pages) is not read, not written and not visible.  Each
  * records RKV_ERR_DEVICE_CHECK in `status`.
  *
+ * What a call writes (pool, outputs, scores, workspace, status word) shares no
+ * byte with anything else it writes or reads, the page table included, except
+ * where the call names two arguments that may be the same (otherwise
+ * RKV_ERR_INVALID_ARG).
+ *
  * Scores, one fp32 weight and one int32 position per token and key head:
  *   weight         device fp32 [n_seqs][H][capacity], the attention weight the
  *                  token received so far (attn_decode_paged adds to it)
@@ -627,8 +632,8 @@ typedef struct {
  * kvcache_paged_insert -- write the newest n_new tokens of every sequence.
  *
  *   k_new, v_new   device bf16 [n_seqs * n_new][H][D], sequence by sequence,
- *                  row stride new_row_stride (elements); must not overlap the
- *                  pool.  Keys as the attention is to read them (rotated).
+ *                  row stride new_row_stride (elements).  Keys as the attention
+ *                  is to read them (rotated).
  *   n_new          tokens per sequence, >= 0 (0 = no-op)
  *   seq_lens       lengths with the new tokens included: row i of sequence s
  *                  becomes token seq_lens[s] - n_new + i; rows that fall
@@ -650,8 +655,7 @@ rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const void* k_new,
  * attn_decode_paged -- attention of the newest Lq tokens of every sequence
  * over its pages, split over the cache's length and joined.
  *
- *   q, o           device bf16 [n_seqs * Lq][Hq][D], row strides in elements;
- *                  o may not overlap q, the pool or the other outputs
+ *   q, o           device bf16 [n_seqs * Lq][Hq][D], row strides in elements
  *   Lq             query tokens per sequence, 1 .. RKV_DECODE_MAX_LQ; query i
  *                  is token c = seq_lens[s] - Lq + i
  *   Hq             query heads, a multiple of cache->H (query head h reads key
@@ -662,8 +666,7 @@ rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const void* k_new,
  *                  + sum over the queries and the query heads of key head h of
  *                  their softmax weight of token j, for j < seq_lens[s]; the
  *                  rest of weight_out is left as it was.  weight_in NULL counts
- *                  as zeros; weight_out may be weight_in, otherwise the two may
- *                  not overlap.
+ *                  as zeros; weight_out may be weight_in.
  *   workspace      device memory, 16-byte aligned, not used by another call
  *                  in flight, at least
  *                  attn_decode_paged_workspace_size(cache, Hq, Lq, weights)
@@ -700,8 +703,8 @@ rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void* q, void* 
  *
  *   seq_lens_out   min(L, budget); may be seq_lens
  *   weight_out, pos_out   the scores of the indices [0, min(L, budget)) after
- *                  the moves; may be weight / pos (both or neither), otherwise
- *                  they may not overlap them.  The rest is left as it was.
+ *                  the moves; may be weight / pos (both or neither).  The rest
+ *                  is left as it was.
  *   budget         >= 1, sinks, recent >= 0
  *   workspace      as for attn_decode_paged,
  *                  kvcache_paged_evict_workspace_size(cache, budget) bytes

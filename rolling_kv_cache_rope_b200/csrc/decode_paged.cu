@@ -990,22 +990,15 @@ extern "C" rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void
   if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return fail(RKV_ERR_INVALID_ARG, "softmax_scale must be > 0");
   if (window < 0 || sinks < 0) return fail(RKV_ERR_INVALID_ARG, "window and sinks must be >= 0");
   if (weight_in && !weight_out) return fail(RKV_ERR_INVALID_ARG, "weight_in without weight_out");
-  if (rows_overlap(o, n_rows, o_row_stride * 2, row * 2, q, n_rows, q_row_stride * 2, row * 2))
-    return fail(RKV_ERR_INVALID_ARG, "o overlaps q");
-  const uint64_t o_bytes = uint64_t((n_rows - 1) * o_row_stride + row) * 2;
-  if (overlaps_pool(cache, o, o_bytes)) return fail(RKV_ERR_INVALID_ARG, "o overlaps the pool");
-  if (overlaps(o, o_bytes, seq_lens, uint64_t(cache->n_seqs) * 4))
-    return fail(RKV_ERR_INVALID_ARG, "o overlaps seq_lens");
   const uint64_t sb = uint64_t(cache->n_seqs) * cache->H * capacity(cache) * 4;
-  if (weight_out) {
-    if (weight_in && weight_in != weight_out && overlaps(weight_in, sb, weight_out, sb))
-      return fail(RKV_ERR_INVALID_ARG, "weight_in and weight_out overlap in part");
-    const uint64_t lb = uint64_t(cache->n_seqs) * 4;
-    if (overlaps(weight_out, sb, seq_lens, lb) || overlaps(weight_out, sb, o, o_bytes) ||
-        overlaps(weight_out, sb, q, uint64_t((n_rows - 1) * q_row_stride + row) * 2) ||
-        overlaps_pool(cache, weight_out, sb))
-      return fail(RKV_ERR_INVALID_ARG, "weight_out overlaps q, o, seq_lens or the pool");
-  }
+  if (weight_in && weight_in != weight_out && overlaps(weight_in, sb, weight_out, sb))
+    return fail(RKV_ERR_INVALID_ARG, "weight_in and weight_out overlap in part");
+  st = check_apart({{"o", o, n_rows, o_row_stride * 2, row * 2}, run_of("weight_out", weight_out, sb),
+                    run_of("the workspace", workspace, std::min(d.bytes, workspace_bytes)), status_of(cache)},
+                   {{"q", q, n_rows, q_row_stride * 2, row * 2}, pool_k(cache), pool_v(cache), table_of(cache),
+                    run_of("seq_lens", seq_lens, uint64_t(cache->n_seqs) * 4),
+                    run_of("weight_in", weight_in == weight_out ? nullptr : weight_in, sb)});
+  if (st != RKV_OK) return st;
   if (!workspace || !aligned16(workspace) || workspace_bytes < d.bytes)
     return fail(RKV_ERR_INVALID_ARG, "workspace must be >= %zu bytes and 16-byte aligned", d.bytes);
   DecodeArgs a;

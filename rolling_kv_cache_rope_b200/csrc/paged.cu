@@ -28,18 +28,35 @@ int sm_count() {
 
 static int64_t page_bytes(const rkv_paged_cache* c) { return int64_t(c->page_tokens) * c->H * kRowBytes; }
 
-bool overlaps_pool(const rkv_paged_cache* c, const void* p, uint64_t bytes) {
-  const int64_t stride = c->page_stride * 2;
-  if (bytes == 0) return false;
-  for (const void* base : {c->k, c->v}) {
-    // the bytes of p as one row of the pool's own stride where they fit one,
-    // so that a neighbour inside the pool's stride is told from an overlap
-    const bool one = bytes <= uint64_t(stride);
-    if (one ? rows_overlap(p, 1, stride, int64_t(bytes), base, c->n_pages, stride, page_bytes(c))
-            : overlaps(p, bytes, base, uint64_t((c->n_pages - 1) * stride + page_bytes(c))))
-      return true;
+Bytes pool_k(const rkv_paged_cache* c) { return {"the pool k", c->k, c->n_pages, c->page_stride * 2, page_bytes(c)}; }
+Bytes pool_v(const rkv_paged_cache* c) { return {"the pool v", c->v, c->n_pages, c->page_stride * 2, page_bytes(c)}; }
+Bytes table_of(const rkv_paged_cache* c) {
+  const int64_t row = int64_t(c->max_pages) * 4;
+  return {"the page table", c->page_table, c->n_seqs, c->n_seqs > 1 ? c->table_stride * 4 : row, row};
+}
+Bytes status_of(const rkv_paged_cache* c) { return run_of("the status word", c->status, 4); }
+
+static bool meet(Bytes a, Bytes b) {
+  if (!a.p || !b.p) return false;
+  // rows that fit one of the other's strides count as a single row of it, so
+  // that a neighbour between its rows is told from an overlap
+  auto fit = [](Bytes& x, const Bytes& y) {
+    const int64_t span = (x.rows - 1) * x.stride + x.width;
+    if (x.stride != y.stride && span <= y.stride) x = {x.name, x.p, 1, y.stride, span};
+  };
+  fit(a, b);
+  fit(b, a);
+  return rows_overlap(a.p, a.rows, a.stride, a.width, b.p, b.rows, b.stride, b.width);
+}
+
+rkv_status check_apart(std::initializer_list<Bytes> writes, std::initializer_list<Bytes> reads) {
+  for (auto w = writes.begin(); w != writes.end(); ++w) {
+    for (const Bytes& r : reads)
+      if (meet(*w, r)) return fail(RKV_ERR_INVALID_ARG, "%s overlaps %s", w->name, r.name);
+    for (auto x = writes.begin(); x != w; ++x)
+      if (meet(*w, *x)) return fail(RKV_ERR_INVALID_ARG, "%s overlaps %s", w->name, x->name);
   }
-  return false;
+  return RKV_OK;
 }
 
 rkv_status check_cache(const rkv_paged_cache* c) {
@@ -619,17 +636,13 @@ extern "C" rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const v
   const int64_t pieces = rows * cache->H * 16;
   if (rows >= (int64_t(1) << 31) || pieces >= (int64_t(1) << 31) - kInsertThreads * kInsertUnroll)
     return fail(RKV_ERR_UNSUPPORTED, "insert too large for one launch");
-  const uint64_t span = uint64_t((rows - 1) * new_row_stride + row) * 2;
-  if (overlaps_pool(cache, k_new, span) || overlaps_pool(cache, v_new, span))
-    return fail(RKV_ERR_INVALID_ARG, "new tokens overlap the pool");
   const uint64_t sb = score_bytes(cache), lb = uint64_t(cache->n_seqs) * 4;
-  for (const void* scores : {static_cast<const void*>(pos), static_cast<const void*>(weight)})
-    if (scores && (overlaps_pool(cache, scores, sb) || overlaps(scores, sb, seq_lens, lb) ||
-                   (next_pos && overlaps(scores, sb, next_pos, lb)) || overlaps(scores, sb, k_new, span) ||
-                   overlaps(scores, sb, v_new, span)))
-      return fail(RKV_ERR_INVALID_ARG, "scores overlap the pool or an input");
-  if (pos && weight && overlaps(pos, sb, weight, sb))
-    return fail(RKV_ERR_INVALID_ARG, "the scores pos and weight overlap");
+  st = check_apart({pool_k(cache), pool_v(cache), run_of("the scores pos", pos, sb), run_of("the scores weight", weight, sb),
+                    status_of(cache)},
+                   {{"new tokens (k_new)", k_new, rows, new_row_stride * 2, row * 2},
+                    {"new tokens (v_new)", v_new, rows, new_row_stride * 2, row * 2},
+                    run_of("seq_lens", seq_lens, lb), run_of("next_pos", next_pos, lb), table_of(cache)});
+  if (st != RKV_OK) return st;
   InsertArgs a;
   a.c = cache_dev(cache);
   a.k_new = static_cast<const uint8_t*>(k_new);
@@ -674,24 +687,17 @@ extern "C" rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const in
     return fail(RKV_ERR_INVALID_ARG, "seq_lens/weight/pos/next_pos and the outputs must be 4-byte aligned");
   if (budget < 1) return fail(RKV_ERR_INVALID_ARG, "budget must be >= 1");
   if (sinks < 0 || recent < 0) return fail(RKV_ERR_INVALID_ARG, "sinks and recent must be >= 0");
-  const uint64_t sb = score_bytes(cache), lb = uint64_t(cache->n_seqs) * 4;
-  if ((seq_lens_out != seq_lens && overlaps(seq_lens_out, lb, seq_lens, lb)) || overlaps(seq_lens_out, lb, next_pos, lb) ||
-      overlaps(seq_lens_out, lb, weight, sb) || overlaps(seq_lens_out, lb, pos, sb) ||
-      overlaps(seq_lens_out, lb, weight_out, sb) || overlaps(seq_lens_out, lb, pos_out, sb) ||
-      overlaps_pool(cache, seq_lens_out, lb))
-    return fail(RKV_ERR_INVALID_ARG, "seq_lens_out overlaps an input or another output");
-  for (const void* out : {static_cast<const void*>(weight_out), static_cast<const void*>(pos_out)})
-    if (overlaps(out, sb, seq_lens, lb) || overlaps(out, sb, next_pos, lb))
-      return fail(RKV_ERR_INVALID_ARG, "weight_out/pos_out overlap seq_lens or next_pos");
   const bool in_place = weight_out == weight;
   if (in_place != (pos_out == pos)) return fail(RKV_ERR_INVALID_ARG, "weight_out and pos_out are in place both or neither");
-  if (overlaps(weight, sb, pos, sb) || overlaps(weight_out, sb, pos_out, sb) ||
-      (!in_place && (overlaps(weight, sb, weight_out, sb) || overlaps(weight, sb, pos_out, sb) ||
-                     overlaps(pos, sb, weight_out, sb) || overlaps(pos, sb, pos_out, sb))))
-    return fail(RKV_ERR_INVALID_ARG, "weight, pos and their outputs overlap");
-  if (overlaps_pool(cache, weight_out, sb) || overlaps_pool(cache, pos_out, sb))
-    return fail(RKV_ERR_INVALID_ARG, "scores overlap the pool");
   const size_t need = kvcache_paged_evict_workspace_size(cache, budget);
+  const uint64_t sb = score_bytes(cache), lb = uint64_t(cache->n_seqs) * 4;
+  st = check_apart({pool_k(cache), pool_v(cache), run_of("seq_lens_out", seq_lens_out, lb), run_of("weight_out", weight_out, sb),
+                    run_of("pos_out", pos_out, sb), run_of("the workspace", workspace, std::min(need, workspace_bytes)),
+                    status_of(cache)},
+                   {run_of("seq_lens", seq_lens_out == seq_lens ? nullptr : seq_lens, lb),
+                    run_of("weight", in_place ? nullptr : weight, sb), run_of("pos", in_place ? nullptr : pos, sb),
+                    run_of("next_pos", next_pos, lb), table_of(cache)});
+  if (st != RKV_OK) return st;
   if (!workspace || !aligned16(workspace) || workspace_bytes < need)
     return fail(RKV_ERR_INVALID_ARG, "workspace must be >= %zu bytes and 16-byte aligned", need);
   const int64_t items = int64_t(cache->n_seqs) * cache->H;

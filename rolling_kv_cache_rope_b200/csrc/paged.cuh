@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -59,8 +60,20 @@ __device__ __forceinline__ uint32_t row_unit(const CacheDev& c, uint32_t page, u
 // ---- host -------------------------------------------------------------------------
 rkv_status check_cache(const rkv_paged_cache* c);
 CacheDev cache_dev(const rkv_paged_cache* c);   // of a checked cache
-// Does [p, p + bytes) share a byte with a page of the pool?
-bool overlaps_pool(const rkv_paged_cache* c, const void* p, uint64_t bytes);
+// Bytes that a call reads or writes: `rows` runs of `width` bytes, `stride`
+// bytes apart; p = null: none.
+struct Bytes {
+  const char* name;
+  const void* p;
+  int64_t rows, stride, width;
+};
+inline Bytes run_of(const char* name, const void* p, uint64_t bytes) { return {name, p, 1, int64_t(bytes), int64_t(bytes)}; }
+Bytes pool_k(const rkv_paged_cache* c);
+Bytes pool_v(const rkv_paged_cache* c);
+Bytes table_of(const rkv_paged_cache* c);
+Bytes status_of(const rkv_paged_cache* c);
+// What a call writes shares no byte with anything else it writes or reads.
+rkv_status check_apart(std::initializer_list<Bytes> writes, std::initializer_list<Bytes> reads);
 int sm_count();
 
 // Allow kernel kKern `bytes` of dynamic shared memory on the current device:
