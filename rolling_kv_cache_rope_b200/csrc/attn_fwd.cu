@@ -1209,7 +1209,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           if (lane == 0 && ok) ok = wait_phase(c, bar(c, B_VFULL + st), n & 1u, 17);
           const int base = tile_at<kWindow>(un, j) * kBN;
           if (!((base + kBN <= un.hi && base >= un.lo) || base + kBN <= un.sink)) {
-            met = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            // the tile's bytes are ordered before the stores of a lane that has
+            // seen its barrier itself (lane 0's phase stays until it reports)
+            met = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0 && wait_warp(c, bar(c, B_VFULL + st), n & 1u, 17);
             if (!met) break;
             window_clear_v(sV + st * kVStageBytes, base, un.lo, un.hi, un.sink);
             __syncwarp();
