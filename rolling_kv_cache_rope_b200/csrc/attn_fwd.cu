@@ -778,8 +778,15 @@ __device__ __noinline__ void window_tile_hidden(uint32_t tS) {
 // Rows of a V tile (at `tile` in shared memory, first key `base`) that no row
 // of the unit sees have weights of zero, and zero times an infinity or a NaN
 // would enter every sum: they are overwritten with zeros (a row is 128
-// contiguous bytes, swizzled only within itself).  By a whole warp.
-__device__ __noinline__ void window_clear_v(uint32_t tile, int base, int lo, int hi, int sink) {
+// contiguous bytes, swizzled only within itself).  By a whole warp, one lane of
+// which has waited for the tile: its phase is complete and stays so until the
+// warp reports, and each lane's own test orders the load's bytes before its
+// stores (waiting with the stop flag and the clock inline took the denoise pass
+// 4% longer).
+__device__ __noinline__ void window_clear_v(uint32_t full, uint32_t parity, uint32_t tile, int base, int lo, int hi,
+                                            int sink) {
+  for (int i = 0; i < (1 << 20) && !ptx::mbar_try_wait(full, parity); ++i) {
+  }
   for (int x = int(threadIdx.x & 31); x < kBN * 8; x += 32) {
     const int key = base + (x >> 3);
     if (!(key < hi && key >= lo) && key >= sink) ptx::sts128(tile + uint32_t(x) * 16u, make_uint4(0u, 0u, 0u, 0u));
@@ -1209,11 +1216,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           if (lane == 0 && ok) ok = wait_phase(c, bar(c, B_VFULL + st), n & 1u, 17);
           const int base = tile_at<kWindow>(un, j) * kBN;
           if (!((base + kBN <= un.hi && base >= un.lo) || base + kBN <= un.sink)) {
-            // the tile's bytes are ordered before the stores of a lane that has
-            // seen its barrier itself (lane 0's phase stays until it reports)
-            met = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0 && wait_warp(c, bar(c, B_VFULL + st), n & 1u, 17);
+            met = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!met) break;
-            window_clear_v(sV + st * kVStageBytes, base, un.lo, un.hi, un.sink);
+            window_clear_v(bar(c, B_VFULL + st), n & 1u, sV + st * kVStageBytes, base, un.lo, un.hi, un.sink);
             __syncwarp();
           }
           if (lane == 0 && ok) ptx::mbar_arrive_cluster(lbar(B_VREADY + st));
