@@ -1765,6 +1765,9 @@ static int64_t plan_units(const rkv_attn_seq* seqs, const rkv_attn_window* windo
   return units;
 }
 
+// Units are numbered in 31 bits, in windowed launches in those below kPartItem.
+static int64_t max_units(const rkv_attn_window* windows) { return windows ? int64_t(kPartItem) : int64_t(1) << 31; }
+
 // The masks of a windowed launch.
 static rkv_status validate_windows(const rkv_attn_seq* seqs, const rkv_attn_window* windows, int32_t n_seqs,
                                    int64_t F) {
@@ -1838,7 +1841,7 @@ static rkv_status attn_launch(const rkv_attn_seq* seqs, const rkv_attn_window* w
       t_hi = std::max<int64_t>(t_hi, int64_t(s.k_t0) + (s.Lk - 1) / F);
     }
   }
-  if (units >= (windows ? int64_t(kPartItem) : int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
+  if (units >= max_units(windows)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   if (t_lo == INT64_MAX) { t_lo = 0; t_hi = -1; }
   const int64_t n_t = t_hi - t_lo + 1;
   const int32_t pairs[3] = {rope->pairs_t, rope->pairs_h, rope->pairs_w};
@@ -2040,7 +2043,7 @@ static rkv_status host_mask(const rkv_attn_seq* seqs, const rkv_attn_window* win
   memset(&p, 0, sizeof(p));
   int order[RKV_MAX_SEQS], where[RKV_MAX_SEQS];
   const int64_t units = plan_units(seqs, windows, n_seqs, H, H_kv, int64_t(rope->grid_h) * rope->grid_w, p, order);
-  if (units >= (int64_t(1) << 31)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
+  if (units >= max_units(windows)) return fail(RKV_ERR_UNSUPPORTED, "too many work units");
   for (int oi = 0; oi < n_seqs; ++oi) where[order[oi]] = oi;
   int64_t off = 0;
   for (int i = 0; i < n_seqs; ++i) {
