@@ -198,9 +198,16 @@ def _rows(t, name):
     import torch
     if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a bf16 CUDA tensor of shape [L, H, D]")
-    if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    return _stride_of_rows(t, t.shape, name)
+
+
+def _stride_of_rows(t, shape, name):
+    """Row stride of t, [L, H, D] with contiguous rows.  Over a dimension of one
+    a stride says nothing: a single row's is H*D."""
+    s = t.stride()
+    if s[2] != 1 or (s[1] != shape[2] and shape[1] != 1):
         raise ValueError(f"{name}: each row must hold H*D contiguous values")
-    return t.stride(0)
+    return s[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rope3d_apply(x, y=None, t0=0, rope=None, stream=None):
@@ -578,10 +585,17 @@ def _row_stride(t, name, shape, index):
     import torch
     if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
         raise ValueError(f"{name} must be a bf16 CUDA tensor of shape {tuple(shape)} on the cache's device")
-    s = t.stride()
-    if s[2] != 1 or s[1] != shape[2]:
-        raise ValueError(f"{name}: each row must hold H*D contiguous values")
-    return s[0]
+    return _stride_of_rows(t, shape, name)
+
+
+def _check_table(t, device):
+    """Row stride of a page table, int32 [n_seqs, max_pages] on ``device``."""
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 2 or t.device != device or 0 in t.shape \
+            or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("page_table must be int32 [n_seqs, max_pages] (at least one of each) with contiguous rows, on "
+                         "the device of k")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 class PagedKVCache:
@@ -596,22 +610,20 @@ class PagedKVCache:
         if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or k.dim() != 4 or not k.is_cuda or not v.is_cuda:
             raise ValueError("k and v must be bf16 CUDA tensors of shape [n_pages, page_tokens, H, D]")
         n_pages, P, H, D = k.shape
-        if v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+        # (over a dimension of one a stride says nothing)
+        of = lambda t: [x for n, x in zip(t.shape, t.stride()) if n > 1]  # noqa: E731
+        if v.shape != k.shape or of(v) != of(k) or v.device != k.device:
             raise ValueError("k and v must share shape, strides and device")
-        if k.stride()[1:] != (H * D, D, 1):
+        if any(n > 1 and x != w for n, x, w in zip(k.shape[1:], k.stride()[1:], (H * D, D, 1))):
             raise ValueError("a page must be contiguous")
-        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != k.device \
-                or page_table.stride(1) != 1:
-            raise ValueError("page_table must be int32 [n_seqs, max_pages] with contiguous rows, on the device of k")
+        table_stride = _check_table(page_table, k.device)
         self.k, self.v, self.page_table = k, v, page_table
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.n_seqs, self.max_pages = page_table.shape
         self.H, self.capacity, self.index = H, self.max_pages * P, k.get_device()
         self._per_seq = torch.Size((self.n_seqs,))
         self._per_token = torch.Size((self.n_seqs, H, self.capacity))
-        # a single page's or sequence's stride says nothing: any will do
         stride = k.stride(0) if n_pages > 1 else P * H * D
-        table_stride = page_table.stride(0) if self.n_seqs > 1 else self.max_pages
         self.c = rkv_paged_cache(k.data_ptr(), v.data_ptr(), stride, n_pages, P, H, D, page_table.data_ptr(),
                                  table_stride, self.n_seqs, self.max_pages, self.status.data_ptr())
         self.ref = ctypes.byref(self.c)
