@@ -627,6 +627,28 @@ class PagedKVCache:
         self.c = rkv_paged_cache(k.data_ptr(), v.data_ptr(), stride, n_pages, P, H, D, page_table.data_ptr(),
                                  table_stride, self.n_seqs, self.max_pages, self.status.data_ptr())
         self.ref = ctypes.byref(self.c)
+        # calls on other streams wait for the zeros of the status word (a capture
+        # runs when it is replayed; what is made in one belongs to it)
+        self._made_on, self._zeroed = _raw_stream(self.index), None
+        if not torch.cuda.is_current_stream_capturing():
+            self._zeroed = torch.cuda.Event()
+            self._zeroed.record(torch.cuda.current_stream(k.device))
+
+    def _stream(self):
+        """Handle of the current stream, on which the status word is zeroed."""
+        handle = _raw_stream(self.index)
+        if handle != self._made_on and self._zeroed is not None:
+            self._after_zeros()
+        return handle
+
+    def _after_zeros(self):
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            return
+        if self._zeroed.query():
+            self._zeroed = None
+        else:
+            torch.cuda.current_stream(self.k.device).wait_event(self._zeroed)
 
     def _ints(self, t, name):
         """Device pointer of an int32 [n_seqs] tensor."""
@@ -675,7 +697,7 @@ def kvcache_paged_insert(cache, k_new, v_new, seq_lens, next_pos=None, pos=None,
                                      cache._ints(seq_lens, "seq_lens"),
                                      None if next_pos is None else cache._ints(next_pos, "next_pos"),
                                      cache._scores(pos, "pos", torch.int32),
-                                     cache._scores(weight, "weight", torch.float32), _raw_stream(cache.index)))
+                                     cache._scores(weight, "weight", torch.float32), cache._stream()))
 
 
 def attn_decode_paged_workspace_size(cache, Hq, Lq=1, weights=False):
@@ -710,7 +732,7 @@ def attn_decode_paged(q, cache, seq_lens, o=None, window=0, sinks=0, softmax_sca
                                   _SCALE if softmax_scale is None else softmax_scale, _i32(window), _i32(sinks),
                                   cache._scores(weight_in, "weight_in", torch.float32),
                                   cache._scores(weight_out, "weight_out", torch.float32), workspace.data_ptr(), size,
-                                  _raw_stream(cache.index)))
+                                  cache._stream()))
     return o
 
 
@@ -742,7 +764,7 @@ def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0,
         lens_in if seq_lens_out is None else cache._ints(seq_lens_out, "seq_lens_out"),
         w_in if weight_out is None else cache._scores(weight_out, "weight_out", torch.float32),
         p_in if pos_out is None else cache._scores(pos_out, "pos_out", torch.int32), workspace.data_ptr(), size,
-        _raw_stream(cache.index)))
+        cache._stream()))
 
 
 def rkv_paged_status(cache, stream=None):
@@ -751,4 +773,4 @@ def rkv_paged_status(cache, stream=None):
     if _elsewhere(cache.index, stream):
         with _on(cache.k, stream):
             return rkv_paged_status(cache)
-    _check(_lib.rkv_paged_status(cache.ref, _raw_stream(cache.index)))
+    _check(_lib.rkv_paged_status(cache.ref, cache._stream()))
