@@ -514,6 +514,8 @@ def attn_fwd_window(seqs, windows, rope, softmax_scale=None, workspace=None, str
     if workspace is None:
         workspace = torch.empty(attn_fwd_varlen_workspace_size(len(seqs), H, D), dtype=torch.uint8,
                                 device=seqs[0].q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the sequences' device")
     _check(_lib.attn_fwd_window(arr, win, len(seqs), H, H_kv, D, float(softmax_scale), ctypes.byref(rope),
                                 workspace.data_ptr(), workspace.nbytes, _raw_stream(index)))
     return workspace

@@ -73,3 +73,15 @@ def test_one_page_a_sequence():
     cache = rkv.PagedKVCache(st.cache.k, st.cache.v, table)
     q = bf16_normal_bits(3, (3, 2, D))
     check_decode(st, q, rkv.attn_decode_paged(to_dev(q), cache, st.lens_dev), SCALE)
+
+
+def test_window_refuses_a_workspace_elsewhere():
+    need_gpu()
+    from rolling_kv_cache_rope_b200 import rkv
+    q, k, v = (to_dev(bf16_normal_bits(10 + i, (70, 2, D))) for i in range(3))
+    s = rkv.AttnSeq(q, k, v, torch.empty_like(q), rope_q=False, rope_k=False, block_frames=1)
+    big = 2 * rkv.attn_fwd_varlen_workspace_size()
+    # (strided or on the host: refused before anything is launched)
+    for ws in (torch.empty(big, dtype=torch.uint8), torch.empty(big, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            rkv.attn_fwd_window([s], [(3, 0)], rkv.make_rope(1, 1), workspace=ws)
