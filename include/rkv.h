@@ -661,7 +661,8 @@ rkv_status kvcache_paged_insert(const rkv_paged_cache* cache, const void* k_new,
  *   Hq             query heads, a multiple of cache->H (query head h reads key
  *                  head h / (Hq / H))
  *   window, sinks  token j <= c is visible iff window == 0 or j > c - window
- *                  or j < sinks (indices in the cache)
+ *                  or j < sinks.  j is the index in the cache, which is the
+ *                  token's place in the stream until an eviction moves tokens
  *   weight_in, weight_out   NULL, or weight_out[s][h][j] = weight_in[s][h][j]
  *                  + sum over the queries and the query heads of key head h of
  *                  their softmax weight of token j, for j < seq_lens[s]; the
@@ -697,9 +698,12 @@ rkv_status attn_decode_paged(const rkv_paged_cache* cache, const void* q, void* 
  * index), budget in all.  Kept tokens below index `budget` stay where they are;
  * the others move, in order, into the places of dropped tokens below `budget`,
  * in order: K and V rows, weight and pos.  A head's tokens are then the indices
- * [0, budget), in no particular order; the attention over them does not depend
- * on it.  Each head keeps its own tokens.  L <= budget: the sequence is left
- * as it is.
+ * [0, budget), in no particular order: attention over all of them does not
+ * depend on it, but attn_decode_paged's window and sinks count indices, not
+ * positions, and after an eviction the last indices are not the newest tokens.
+ * An evicted cache is attended with window = 0: sinks and recent here are its
+ * window.  Each head keeps its own tokens.  L <= budget: the sequence is left as
+ * it is.
  *
  *   seq_lens_out   min(L, budget); may be seq_lens
  *   weight_out, pos_out   the scores of the indices [0, min(L, budget)) after

@@ -711,7 +711,8 @@ def attn_decode_paged(q, cache, seq_lens, o=None, window=0, sinks=0, softmax_sca
     """Attention of the newest Lq tokens of every sequence over its pages: q
     bf16 [n_seqs * Lq, Hq, 128], sequence by sequence; ``seq_lens`` counts
     them.  ``window`` / ``sinks``: a token sees the last ``window`` tokens and
-    the first ``sinks`` (0 = all).  ``weight_out`` = ``weight_in`` + the
+    the first ``sinks`` (0 = all), by index in the cache (not for an evicted
+    one, whose order is no longer the stream's).  ``weight_out`` = ``weight_in`` + the
     attention weight each cached token received (may be the same tensor).
     Returns o (allocated here when None)."""
     import torch
@@ -748,7 +749,8 @@ def kvcache_paged_evict_workspace_size(cache, budget):
 def kvcache_paged_evict(cache, seq_lens, weight, pos, next_pos, budget, sinks=0, recent=0, seq_lens_out=None,
                         weight_out=None, pos_out=None, workspace=None, stream=None):
     """Cut every sequence to ``budget`` tokens per key head, dropping those of
-    the least accumulated weight (see rkv.h).  The outputs default to their
+    the least accumulated weight (see rkv.h); what is left is in no particular
+    order, so it is attended without a window.  The outputs default to their
     inputs (in place)."""
     import torch
     if _elsewhere(cache.index, stream):
