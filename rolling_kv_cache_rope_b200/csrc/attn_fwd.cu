@@ -144,7 +144,7 @@ struct Params {
   // 512 / pack rows of each, and its four 128-row sub-tiles belong to `pack`
   // heads, so that a window's tiles serve rows that see nearly the same keys
   // (a causal window of 1,024 over 16 / 4 heads and 4,097 rows: 70 us, 88
-  // without)
+  // without; 12 / 6 heads, 2,000 rows and a window of 4,000: 91, 98)
   int32_t pack;
   // windowed: items that are parts of a unit, with their entries [kt0, kt1) of
   // the unit's list of tiles
@@ -718,9 +718,10 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFF
 // tile's, and the sum of the P.  m: the running max so far; P is taken against
 // the new one where it moves.  Out of line, in loops over 32 scores at a time
 // read from TMEM twice: the hot loop's code and registers stay as they are
-// without it (inlined, the instruction cache missed 2.7 times as often and
-// the denoise pass took 20% longer).  A warp's 32 rows cut through one or two of
-// the four chunks; the others take no select.
+// without it (inlined, the denoise pass with a window of 4 blocks and 1 takes
+// 3.38 ms against 3.14, 7,800 x 9,360 with the same window 553 us against 529;
+// launches of a few tiles a unit gain up to 4%, 24.2 -> 23.3 us).  A warp's 32
+// rows cut through one or two of the four chunks; the others take no select.
 __device__ __noinline__ float2 window_tile(uint32_t tS, uint32_t row, int kbase, float scale_log2, float m) {
   const uint4 x = ptx::lds128(row);
   auto chunk = [&](uint32_t (&r)[32], int ch) {
@@ -1578,8 +1579,9 @@ static bool build_schedule(Params& p, int64_t units, int max_clusters) {
 // the busiest pair's work.  Fills p.use_sched, p.sched_off, p.sched and the
 // parts; `split` lists the split units, with their first part and number of
 // parts.  `slots`: partial results the workspace holds.  One head of 4,753 rows
-// over three frames of 30 x 51 takes 69 us (with halves only 115), the denoise
-// pass with a window of four blocks 3.30 ms (unsplit 3.41).
+// over three frames of 30 x 51 takes 41 us (unsplit 109), two heads of 1,950 rows
+// with a window of three frames 36.5 (64), the denoise pass with a window of four
+// blocks 3.14 ms (3.33); units that fill the machine alike are left whole.
 struct WindowSplit {
   int n = 0, parts = 0;   // split units, parts of all of them
   int unit[kMaxSplit], part0[kMaxSplit], count[kMaxSplit];
@@ -1649,7 +1651,12 @@ static WindowSplit build_window_schedule(Params& p, int64_t units, int max_clust
     return worst + (s.parts > 0 ? 2 : 0);
   };
   int32_t best = 0, least = assign(0, false);
-  // (many units leave few slots for each: halves will do)
+  // Parts of a half, a quarter, a ninth or a sixteenth of the longest unit are
+  // tried and the shortest plan is taken.  600 rows of one head over 32,760
+  // keys: 552 us unsplit, 299 with halves only, 162 with quarters, 68 with all
+  // four; with 3, 6, 12 and 24 beside them 62, the other launches measured the
+  // same, for twice the planning.  (Many units leave few slots for each: halves
+  // will do.)
   for (int div : {2, 4, 9, 16}) {
     const int32_t most = (whole[0].cost + div - 1) / div;
     if (most < 2 || slots < 2 || (div > 2 && n > 2 * max_clusters)) break;

@@ -13,10 +13,12 @@
 //
 // Bound: every visible K and V row is read once, 512 bytes for 4 * 128 flops
 // per query row; with at most 32 rows to a key head the kernel is bound by
-// HBM.  A tcgen05 tile has at least 64 query rows, most of them empty here, and
-// needs its operands in whole swizzled tiles where pages end anywhere; the
-// warp-level m16n8k16 product takes 16 rows and is far from its own limit at
-// this bandwidth (16 keys of a head cost 32 of them per 8 KB).
+// HBM.  With the queries on M a tcgen05 tile has at least 64 rows, most of them
+// empty here; the warp-level m16n8k16 product takes 16 rows and is far from its
+// own limit at this bandwidth (16 keys of a head cost 32 of them per 8 KB).  From
+// 17 rows on its chains bound the kernel instead (figures at decode_shape); keys
+// on M and rows on N would leave no row of a tcgen05 tile empty and is not built:
+// it needs every page's rows in swizzled tiles and P^T through shared memory.
 //
 // Split: the key rows of all (sequence, key head, row block) items, in steps
 // of 64 or 32 keys, form one list of T steps, and each of C blocks takes T / C of
@@ -38,11 +40,12 @@
 // a bad page) is not read but zero-filled, so nothing it holds can enter a sum.
 //
 // Measured (GPU time alone): one stream of 32,760 tokens, 12 heads, 42 us for
-// 201 MB; 64 streams of 1 to 8,192 tokens, 32 / 8 heads, 187 us for 1,112 MB
-// (5.9 TB/s).  About 10 us of either do not shrink with the bytes: finding the
-// steps 2, the first copies 3, merging the warps 2, the join 4; and the SMs end
-// 15 to 20% apart, although each reads the same bytes.  With weights (24 streams of
-// 2,000 to 4,097 tokens, 24 / 8 heads, 317 MB): 68.6 us.
+// 201 MB; 64 streams of 1 to 8,192 tokens, 32 / 8 heads, 186 to 194 us from one
+// GPU to the next for 1,112 MB (5.7 to 6.0 TB/s).  About 10 us of either do not
+// shrink with the bytes: finding the steps 2, the first copies 3, merging the
+// warps 2, the join 4; and the SMs end 15 to 20% apart, although each reads the
+// same bytes.  With weights (24 streams of 2,000 to 4,097 tokens, 24 / 8 heads,
+// 317 MB): 68 us.
 #include <math.h>
 
 #include <algorithm>
@@ -660,9 +663,11 @@ __device__ __forceinline__ int64_t part_row(const DecodeArgs& a, int b0, int slo
   return (int64_t(b0 + i) * 2 + (i == 0 ? slot : 0)) * a.rows_blk + r;
 }
 
-// (blocks per SM: without weights the parts of many rows want four, 50 us
-// against 52 for four query tokens of 16 streams; with weights 64 registers
-// spill, 71.1 us against 68.6)
+// (blocks per SM: four without weights, in 64 registers.  Four query tokens of
+// 16 streams, 32 rows: 43.1 us, with three blocks 43.7; but 8 rows of 3 streams
+// of 31,012 tokens, one key head, take 37 where three blocks take 26, because the
+// path over many parts spills.  Three with weights: 24 streams measure 66.1
+// either way, 40 rows of one stream 67.4 and with four blocks 62.)
 template <bool kWeights>
 __global__ void __launch_bounds__(kJoinThreads, kWeights ? 3 : 4) decode_join_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float4 part[kJoinThreads / 32][32];
@@ -674,7 +679,12 @@ __global__ void __launch_bounds__(kJoinThreads, kWeights ? 3 : 4) decode_join_ke
   // the blocks after it.  A row is joined by `per` warps (all eight where there
   // is one row), each with every per-th part; they meet in order in shared
   // memory.  The first parts are loaded beside the record that says whether and
-  // how many there are: what is not a part is not used.
+  // how many there are: what is not a part is not used.  One row: 42.2 us for a
+  // stream of 32,760 tokens and 12 heads, 42.9 with one warp a row.  From five
+  // rows on a warp has a row to itself: 8 rows of 16 streams of 2,000 tokens 32.4
+  // us, with eight warps a row 35.9, 32 rows 43.2 and 57.9.  Where few key heads
+  // leave an item a hundred parts it is the slower way, 37 us against 21.7 (3
+  // streams of 31,012 tokens, one key head, 8 rows).
   const int per = a.rows_blk == 1 ? 8 : (a.rows_blk == 2 ? 4 : (a.rows_blk <= 4 ? 2 : 1));
   const int b0 = blockIdx.x, w0 = warp % per, r = int(blockIdx.y) * (8 / per) + warp / per;
   const bool row_ok = r < a.rows_blk;

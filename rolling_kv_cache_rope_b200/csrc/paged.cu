@@ -181,22 +181,30 @@ __global__ void __launch_bounds__(kInsertThreads) paged_insert_kernel(const __gr
 // Bound: reading weight and pos (8 bytes a token and key head) and, out of
 // place, writing them; then the rows that move (1 KB each).  Two ways to find
 // the tokens to drop, by how many there are (E = L - budget):
-//   E <= kFew   E rounds of a block-wide minimum over (key, index), about 0.1 us
-//               a round, and the block moves the rows itself: a decode step's
-//               eviction is one launch.  48 streams x 8 heads x 4,096 tokens:
-//               8.5 us for E = 1 (25.6 MB: 3.0 TB/s, the dependent loads of one
-//               head's step bound it), 24.6 for E = 16, where the way below
-//               takes 31 to 34 for any E
+//   E <= kFew and a block has the head to itself (no cluster, see below): E
+//               rounds of a block-wide minimum over (key, index), about 1 us a
+//               round, and the block moves the rows itself.  48 streams x 8 heads
+//               x 4,096 tokens: 8.7 us for E = 1 (25.6 MB: 3.0 TB/s, the dependent
+//               loads of one head's step bound it), 24.8 for E = 16, 24.8 the
+//               way below for E = 17
 //   otherwise   radix selection of the budget-th largest key, 11 bits a pass,
 //               then lists of the places that fall free and of the tokens that
 //               move into them; a second launch moves the rows over all SMs
-//               (24 heads of 32,760 tokens cut to 7,800: 54.5 us, of them 22
-//               for the selection, a chain of passes, and 21 for the rows,
-//               which move at 6.9 TB/s; by the selecting blocks themselves the
-//               whole took 66 against 58 at that time)
+//               (24 heads of 32,760 tokens cut to 7,800: 55 us, of them 22
+//               for the selection, a chain of passes, and 21 for the rows, which
+//               move at 6.9 TB/s, part of it out of L2; by the selecting blocks
+//               themselves the whole took 66 against 58 at that time)
+// The second launch is left out where no sequence can have more than kFew
+// tokens to drop (capacity - budget <= kFew), blocks have heads to themselves
+// and the new lengths are apart from the old; a step's eviction under pages that
+// leave more room behind the budget launches it with nothing to move (9.9 us
+// against 8.7).
 // A head's tokens are shared out over a cluster of blocks where there are too
 // few heads and sequences to fill the machine; the blocks' histograms and
-// counts meet in distributed shared memory.
+// counts meet in distributed shared memory.  That is the faster way for many
+// tokens to drop (figures where the host decides) and the slower for one or a
+// few: 76 heads of 2,542 tokens, one dropped, 13 us against 4.9; 12 heads of
+// 4,097 12.3 against 5.4.
 // ---------------------------------------------------------------------------
 struct EvictArgs {
   CacheDev c;
@@ -723,7 +731,8 @@ extern "C" rkv_status kvcache_paged_evict(const rkv_paged_cache* cache, const in
   a.lens_here = seq_lens_out != seq_lens;
   // blocks a head: one where the heads and sequences alone fill the machine
   // (or a head is short), else up to eight: 24 heads cut from 32,760 to 7,800
-  // tokens took 58 us, with one block each 103
+  // tokens (uniform weights) 63 us, with one block each 112; 12 heads from 4,097 to
+  // 2,000 17.2 and 19.4; 76 heads from 2,542 to 1,200 30.1 and 26.5
   const int sms = sm_count();
   a.cluster = 1;
   while (a.cluster < kMaxCluster && items * a.cluster * 2 <= 2 * sms && capacity(cache) >= 2048 * int64_t(a.cluster))
