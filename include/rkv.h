@@ -399,7 +399,8 @@ rkv_status rkv_attn_noalloc_status(void* stream);
  * softmax statistics and sums are fp32.
  * Errors: those of attn_fwd_varlen, plus RKV_ERR_INVALID_ARG for NULL windows,
  * block_frames < 1, window_blocks or sink_blocks < 0, H not a multiple of H_kv,
- * and RKV_ERR_UNSUPPORTED for a query row in frame 2^31 - 1 or later.
+ * and RKV_ERR_UNSUPPORTED for a query row in frame 2^31 - 1 or later or for 2^30
+ * or more units.
  */
 typedef struct {
   int32_t window_blocks; /* blocks a row sees, its own included; 0 = all      */

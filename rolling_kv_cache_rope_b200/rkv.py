@@ -632,9 +632,10 @@ class PagedKVCache:
         # calls on other streams wait for the zeros of the status word (a capture
         # runs when it is replayed; what is made in one belongs to it)
         self._made_on, self._zeroed = _raw_stream(self.index), None
-        if not torch.cuda.is_current_stream_capturing():
-            self._zeroed = torch.cuda.Event()
-            self._zeroed.record(torch.cuda.current_stream(k.device))
+        with torch.cuda.device(k.device):
+            if not torch.cuda.is_current_stream_capturing():
+                self._zeroed = torch.cuda.Event()
+                self._zeroed.record()
 
     def _stream(self):
         """Handle of the current stream, on which the status word is zeroed."""
